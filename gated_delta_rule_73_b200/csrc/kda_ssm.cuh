@@ -1,0 +1,142 @@
+// kda_ssm.cuh -- what the selective scan's forward and backward kernels share: the lanes'
+// layout, the loads of a tile of 16 tokens, the reductions between lanes.
+#pragma once
+#include "kda_layers_internal.h"
+#include "kda_rows.cuh"
+
+#include <initializer_list>
+
+namespace kda {
+
+struct SsmP {
+    const void *u, *dt, *Bm, *Cm, *z, *dout;
+    const float *A, *Dskip, *dt_bias, *h0, *dh_T;
+    void *out, *du, *ddt, *dz;
+    float *h_T, *dh0;
+    Seqs q;
+    int D, G, Dg, cpg, nblk;   // channels, groups, channels a group, channel blocks a group, in all
+    int softplus, vec, vecb;   // vec: channel vectors of u, dt, z, out aligned; vecb: B, C
+    int L;                     // rows a span
+    long long ld_u, ld_dt, ld_z, ld_B, ld_C, ld_out, slots;
+    // workspace: states and their gradients at the spans' seams [slots][D][N], the spans' sums of
+    // delta [slots][D], partial sums (backward)
+    float *hst, *gst, *sdel, *part_A, *part_D, *part_bias, *part_BC;
+};
+
+constexpr int kSsmThreads = 256;
+constexpr int kTile = 16;       // tokens a tile
+
+// A channel's N states lie on NQ = N / 4 neighbouring lanes, four a lane; a block holds CH
+// channels.  For the tile's loads 16 threads share a token, EPT channels each.
+template <int N>
+struct SsmShape {
+    static constexpr int NQ = N / 4;
+    static constexpr int CH = kSsmThreads / NQ;
+    static constexpr int EPT = CH / 16;
+    static constexpr int BE = N >= 16 ? N / 16 : 1;   // values of B (and of C) a thread loads
+    // a row of CH sums in shared memory: the pad spreads the NQ rows that a warp writes at once
+    // over the banks
+    static constexpr int ROW = CH + 32 / NQ;
+};
+
+// Sum of v[i] over the NQ lanes of a channel; lane q gets the sum of v[q].
+template <int NQ>
+__device__ __forceinline__ float reduce_states(float (&v)[NQ], int q) {
+#pragma unroll
+    for (int o = NQ / 2; o >= 1; o >>= 1) {
+        const bool up = q & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    return v[0];
+}
+
+// The raw values of one tensor that a thread loads for its token and EPT channels.
+template <typename T, int EPT>
+__device__ __forceinline__ Raw<T, EPT> load_tile(const void *p, long long row, long long ld, int c, int left,
+                                                 bool ok, int vec) {
+    const T *a = (const T *)p + row * ld + c;
+    if (ok && vec && left >= EPT) return load_raw<T, EPT>(a);
+    return load_part<T, EPT>(a, ok ? left : 0);
+}
+
+// A block's span and channels.
+struct SsmBlock {
+    Span sp;
+    long long slot;
+    int blk, g, cin;   // block of channels, its group, first channel within the group
+};
+__device__ __forceinline__ SsmBlock ssm_block(const SsmP &a, int CH) {
+    SsmBlock b;
+    b.slot = blockIdx.x / a.nblk;
+    b.blk = blockIdx.x % a.nblk;
+    b.g = b.blk / a.cpg;
+    b.cin = (b.blk % a.cpg) * CH;
+    b.sp = span_at(a.q, b.slot, a.L);
+    return b;
+}
+
+// B and C of a tile: loads into registers, then FP32 into shared memory [kTile][N].
+template <typename T, int N>
+struct BcTile {
+    static constexpr int BE = SsmShape<N>::BE, PER = N / BE;
+    Raw<T, BE> b, c;
+    __device__ __forceinline__ void fetch(const SsmP &a, long long r0, int n, int g, bool with_c) {
+        const int t = threadIdx.x / PER, i = (threadIdx.x % PER) * BE;
+        const bool ok = t < n && t < kTile;
+        const T *pb = (const T *)a.Bm + (r0 + t) * a.ld_B + g * N + i;
+        b = ok && a.vecb ? load_raw<T, BE>(pb) : load_part<T, BE>(pb, ok ? BE : 0);
+        if (with_c) {
+            const T *pc = (const T *)a.Cm + (r0 + t) * a.ld_C + g * N + i;
+            c = ok && a.vecb ? load_raw<T, BE>(pc) : load_part<T, BE>(pc, ok ? BE : 0);
+        }
+    }
+    __device__ __forceinline__ void put(float *sB, float *sC) {
+        const int t = threadIdx.x / PER, i = (threadIdx.x % PER) * BE;
+        if (t < kTile) {
+            float v[BE];
+            widen<T, BE>(b, v);
+#pragma unroll
+            for (int k = 0; k < BE; ++k) sB[t * N + i + k] = v[k];
+            if (sC) {
+                widen<T, BE>(c, v);
+#pragma unroll
+                for (int k = 0; k < BE; ++k) sC[t * N + i + k] = v[k];
+            }
+        }
+    }
+};
+
+// Fills in sizes and layout; the kernels' own pointers are the launchers' to set.
+template <int N>
+SsmP ssm_params(const SsmArgs &a, int L) {
+    using S = SsmShape<N>;
+    SsmP p = {};
+    p.u = a.u; p.dt = a.dt; p.Bm = a.Bm; p.Cm = a.Cm; p.z = a.z; p.dout = a.dout;
+    p.A = a.A; p.Dskip = a.Dskip; p.dt_bias = a.dt_bias; p.h0 = a.h0; p.dh_T = a.dh_T;
+    p.out = a.out; p.du = a.du; p.ddt = a.ddt; p.dz = a.dz; p.h_T = a.h_T; p.dh0 = a.dh0;
+    p.q.cu = a.cu; p.q.S = a.S; p.q.T = a.T;
+    p.D = a.D; p.G = a.G; p.Dg = a.D / a.G;
+    p.cpg = (p.Dg + S::CH - 1) / S::CH;
+    p.nblk = p.cpg * a.G;
+    p.softplus = a.softplus;
+    long long ld = a.ld_u | a.ld_dt | (a.z ? a.ld_z : 0) | a.ld_out | p.Dg;
+    for (const void *r : {a.u, a.dt, a.z, (const void *)a.out, a.dout}) ld |= elements(r, a.bf16);
+    const int most = a.bf16 ? (S::EPT < 8 ? S::EPT : 8) : (S::EPT < 4 ? S::EPT : 4);
+    // a whole vector of EPT channels is in the group, or none of it, and is aligned
+    p.vec = ld % most == 0 && p.Dg % S::EPT == 0;
+    p.vecb = (a.ld_B | a.ld_C | elements(a.Bm, a.bf16) | elements(a.Cm, a.bf16)) % S::BE == 0;
+    p.L = L;
+    p.ld_u = a.ld_u; p.ld_dt = a.ld_dt; p.ld_z = a.ld_z; p.ld_B = a.ld_B; p.ld_C = a.ld_C; p.ld_out = a.ld_out;
+    p.slots = span_slots(a.cu != nullptr, a.S, a.T, L);
+    return p;
+}
+
+// Start states of the spans (hst) from the spans' own ends, and, where gst is set, the
+// gradients at the spans' ends from the spans' own gradients at their starts.
+cudaError_t launch_ssm_seams(const SsmP &p, int N, cudaStream_t st);
+
+}  // namespace kda

@@ -1,0 +1,473 @@
+"""Binding of the operators of ``include/kda_layers.h``: short convolution, selective scan, block norm.
+
+As ``kda.py``: argument checks and marshalling only, no arithmetic and no fallback.  The ``kda_*``
+functions take every output; the functions without the prefix allocate outputs and workspaces
+with torch and return them.  Sequences are dense (``x [B, T, D]``) or packed (``x [rows, D]`` and
+``cu_seqlens`` int32 ``[B + 1]`` on the device); a row tensor may be a column range of a wider one
+(its last dimension contiguous, its rows evenly spaced).  Outputs that these functions allocate
+for packed sequences hold zeros in rows of no sequence; outputs that are passed in keep theirs.
+
+All tensors of a call live on one device; work goes to ``stream`` or to that device's current one,
+whichever device is current in the calling thread.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import kda as _kda
+from .kda import KDA_BF16, KDA_F32, KdaError, kda_opts
+
+_lib = _kda._lib
+_ip, _ll, _vp, _sz = ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p, ctypes.c_size_t
+
+
+class kda_conv_dims(ctypes.Structure):
+    _fields_ = [("B", _ip), ("T", _ip), ("D", _ip), ("K", _ip), ("silu", _ip), ("cu_seqlens", _vp),
+                ("zero_rest", _ip), ("ld_x", _ll), ("ld_y", _ll), ("ld_dx", _ll)]
+
+
+class kda_ssm_dims(ctypes.Structure):
+    _fields_ = [("B", _ip), ("T", _ip), ("D", _ip), ("N", _ip), ("G", _ip), ("dt_softplus", _ip),
+                ("cu_seqlens", _vp), ("zero_rest", _ip), ("ld_u", _ll), ("ld_dt", _ll), ("ld_z", _ll),
+                ("ld_B", _ll), ("ld_C", _ll), ("ld_out", _ll)]
+
+
+class kda_norm_dims(ctypes.Structure):
+    _fields_ = [("rows", _ip), ("D", _ip), ("eps", ctypes.c_float), ("ld_res", _ll), ("ld_block", _ll),
+                ("ld_gate", _ll)]
+
+
+def _declare():
+    op = ctypes.POINTER(kda_opts)
+    cd, sd, nd = (ctypes.POINTER(s) for s in (kda_conv_dims, kda_ssm_dims, kda_norm_dims))
+    for name, pointers, dims in (("kda_short_conv_fwd", 6, cd), ("kda_short_conv_bwd", 10, cd),
+                                 ("kda_short_conv_step", 6, cd), ("kda_ssm_scan_fwd", 11, sd),
+                                 ("kda_ssm_scan_bwd", 20, sd), ("kda_ssm_step", 11, sd),
+                                 ("kda_block_norm_fwd", 8, nd), ("kda_block_norm_bwd", 14, nd)):
+        f = getattr(_lib, name)
+        f.argtypes = [_vp] * pointers + [dims, op, _vp]
+        f.restype = _ip
+    for name, dims in (("kda_short_conv_bwd_workspace_bytes", cd), ("kda_ssm_scan_fwd_workspace_bytes", sd),
+                       ("kda_ssm_scan_bwd_workspace_bytes", sd), ("kda_block_norm_bwd_workspace_bytes", nd)):
+        f = getattr(_lib, name)
+        f.argtypes = [dims, op]
+        f.restype = _sz
+
+
+_declare()
+_F32 = torch.float32
+
+
+# ------------------------------------------------------------------ argument checks
+class _Call:
+    """Checks the tensors of one call: type, shape, device, layout; collects their addresses."""
+    __slots__ = ("dtype", "device", "lead")
+
+    def __init__(self, x, name, lead):
+        if not isinstance(x, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not x.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        self.dtype, self.device, self.lead = x.dtype, x.device, lead
+
+    def flat(self, t, name, shape, dtype=None):
+        """Address of a contiguous tensor of this shape; None stays None."""
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != (dtype or self.dtype):
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype or self.dtype}")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def rows(self, t, name, tail):
+        """(address, row stride) of a row tensor [*lead, *tail]; (None, 0) for None."""
+        if t is None:
+            return None, 0
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != self.dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {self.dtype}")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
+        if t.shape != self.lead + tail:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {self.lead + tail}")
+        if t.is_contiguous():
+            return t.data_ptr(), 0
+        st, lead = t.stride(), len(self.lead)
+        width = math.prod(tail)
+        # the row itself is contiguous
+        want = 1
+        for n, s in zip(reversed(tail), reversed(st[lead:])):
+            if n != 1 and s != want:
+                raise ValueError(f"{name}: the values of a row must be contiguous (strides {st})")
+            want *= n
+        # rows evenly spaced: dimensions of one element say nothing about it
+        ld, span = None, 1
+        for n, s in zip(reversed(self.lead), reversed(st[:lead])):
+            if n != 1:
+                if ld is None:
+                    if s % span:
+                        raise ValueError(f"{name}: rows must be evenly spaced (strides {st})")
+                    ld = s // span
+                elif s != ld * span:
+                    raise ValueError(f"{name}: rows must be evenly spaced (strides {st})")
+            span *= n
+        if ld is None:
+            ld = width
+        if ld < width:
+            raise ValueError(f"{name}: rows overlap (strides {st})")
+        return t.data_ptr(), ld
+
+
+def _opts(dtype, workspace=None, device=None):
+    o = kda_opts()
+    if dtype == torch.bfloat16:
+        o.dtype = KDA_BF16
+    elif dtype == _F32:
+        o.dtype = KDA_F32
+    else:
+        raise TypeError(f"unsupported activation dtype {dtype}; use bfloat16 or float32")
+    o.scale = 1.0
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError("workspace must be a torch.Tensor")
+        if workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        o.workspace = workspace.data_ptr()
+        o.workspace_bytes = workspace.numel() * workspace.element_size()
+    return o
+
+
+def _launch(fn, call, args, dims, opts, stream):
+    """Runs the C call on the tensors' device."""
+    dev = call.device
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, expected {dev}")
+    if torch.cuda.current_device() == dev.index:
+        h = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+        st = fn(*args, dims, opts, h)
+    else:
+        with torch.cuda.device(dev):
+            h = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+            st = fn(*args, dims, opts, h)
+    if st != 0:
+        raise KdaError(fn.__name__, st)
+
+
+def _workspace(nbytes, device, stream):
+    """Scratch for one call, from the memory of the stream that uses it."""
+    if nbytes == 0:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _sequences(x, cu_seqlens, D_dims=1):
+    """(lead, B, T) of a row tensor; checks cu_seqlens."""
+    lead = x.shape[:-D_dims]
+    if cu_seqlens is None:
+        if len(lead) != 2:
+            raise ValueError(f"expected [B, T, ...] without cu_seqlens, got shape {tuple(x.shape)}")
+        return lead, lead[0], lead[1]
+    if len(lead) != 1:
+        raise ValueError(f"expected [rows, ...] with cu_seqlens, got shape {tuple(x.shape)}")
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 \
+            or cu_seqlens.shape[0] < 1:
+        raise TypeError("cu_seqlens must be an int32 tensor of B + 1 values")
+    return lead, cu_seqlens.shape[0] - 1, lead[0]
+
+
+def _sizes(*sizes):
+    """The C structures hold sizes as int."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"sizes {sizes} do not fit an int")
+
+
+def _cu(call, cu_seqlens):
+    return None if cu_seqlens is None else call.flat(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32)
+
+
+# ------------------------------------------------------------------ short convolution
+def _conv_call(x, w, cu_seqlens, silu, zero_rest, step=False):
+    if not isinstance(x, torch.Tensor) or not isinstance(w, torch.Tensor):
+        raise TypeError("x and w must be torch.Tensors")
+    if w.dim() != 2:
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected [D, K]")
+    if step:
+        if x.dim() != 2:
+            raise ValueError(f"x has shape {tuple(x.shape)}, expected [B, D]")
+        lead, B, T = x.shape[:1], x.shape[0], 1
+    else:
+        lead, B, T = _sequences(x, cu_seqlens)
+    call = _Call(x, "x", lead)
+    D, K = x.shape[-1], w.shape[1]
+    _sizes(B, T, D, K)
+    d = kda_conv_dims(B=B, T=T, D=D, K=K, silu=bool(silu), cu_seqlens=_cu(call, cu_seqlens), zero_rest=bool(zero_rest))
+    return call, d, (B, K - 1, D), (D, K)
+
+
+def kda_short_conv_fwd(x, w, bias, state0, y, state_T, *, cu_seqlens=None, silu=True, zero_rest=False,
+                       stream=None) -> None:
+    """Call ``kda_short_conv_fwd``; x, y [B,T,D] or packed [rows,D], w [D,K], bias [D], states [B,K-1,D]."""
+    call, d, state, taps = _conv_call(x, w, cu_seqlens, silu, zero_rest)
+    px, d.ld_x = call.rows(x, "x", (d.D,))
+    py, d.ld_y = call.rows(y, "y", (d.D,))
+    args = (px, call.flat(w, "w", taps), call.flat(bias, "bias", (d.D,)), call.flat(state0, "state0", state), py,
+            call.flat(state_T, "state_T", state))
+    _launch(_lib.kda_short_conv_fwd, call, args, d, _opts(x.dtype), stream)
+
+
+def kda_short_conv_bwd_workspace_bytes(x, w, *, cu_seqlens=None) -> int:
+    """Workspace bytes ``kda_short_conv_bwd`` needs for these tensors."""
+    _, d, _, _ = _conv_call(x, w, cu_seqlens, True, False)
+    return int(_lib.kda_short_conv_bwd_workspace_bytes(d, _opts(x.dtype)))
+
+
+def kda_short_conv_bwd(x, w, bias, state0, dy, dstate_T, dx, dw, dbias, dstate0, workspace, *, cu_seqlens=None,
+                       silu=True, zero_rest=False, stream=None) -> None:
+    """Call ``kda_short_conv_bwd``: gradients of <dy, y> + <dstate_T, state_T> of ``kda_short_conv_fwd``."""
+    call, d, state, taps = _conv_call(x, w, cu_seqlens, silu, zero_rest)
+    px, d.ld_x = call.rows(x, "x", (d.D,))
+    py, d.ld_y = call.rows(dy, "dy", (d.D,))
+    pdx, d.ld_dx = call.rows(dx, "dx", (d.D,))
+    args = (px, call.flat(w, "w", taps), call.flat(bias, "bias", (d.D,)), call.flat(state0, "state0", state), py,
+            call.flat(dstate_T, "dstate_T", state, _F32), pdx, call.flat(dw, "dw", taps, _F32),
+            call.flat(dbias, "dbias", (d.D,), _F32), call.flat(dstate0, "dstate0", state, _F32))
+    _launch(_lib.kda_short_conv_bwd, call, args, d, _opts(x.dtype, workspace, call.device), stream)
+
+
+def kda_short_conv_step(x, w, bias, state, state_out, y, *, silu=True, stream=None) -> None:
+    """Call ``kda_short_conv_step``; x, y [B,D], state, state_out [B,K-1,D] (state_out may be state)."""
+    call, d, shape, taps = _conv_call(x, w, None, silu, False, step=True)
+    px, d.ld_x = call.rows(x, "x", (d.D,))
+    py, d.ld_y = call.rows(y, "y", (d.D,))
+    args = (px, call.flat(w, "w", taps), call.flat(bias, "bias", (d.D,)), call.flat(state, "state", shape),
+            call.flat(state_out, "state_out", shape), py)
+    _launch(_lib.kda_short_conv_step, call, args, d, _opts(x.dtype), stream)
+
+
+def short_conv_fwd(x, w, bias=None, state0=None, *, cu_seqlens=None, silu=True, y=None, stream=None):
+    """Causal depthwise convolution with SiLU; returns (y, state_T)."""
+    zero = y is None and cu_seqlens is not None
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    B = x.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    state_T = torch.empty((B, w.shape[1] - 1, x.shape[-1]), dtype=x.dtype, device=x.device)
+    kda_short_conv_fwd(x, w, bias, state0, y, state_T, cu_seqlens=cu_seqlens, silu=silu, zero_rest=zero, stream=stream)
+    return y, state_T
+
+
+def short_conv_bwd(x, w, bias, state0, dy, dstate_T=None, *, cu_seqlens=None, silu=True, workspace=None,
+                   stream=None):
+    """Gradients of ``short_conv_fwd``; returns (dx, dw, dbias, dstate0), None for what was not passed."""
+    if workspace is None:
+        workspace = _workspace(kda_short_conv_bwd_workspace_bytes(x, w, cu_seqlens=cu_seqlens), x.device, stream)
+    e = lambda t, dtype=_F32: None if t is None else torch.empty(t.shape, dtype=dtype, device=x.device)  # noqa: E731
+    dx, dw, dbias, dstate0 = e(x, x.dtype), e(w), e(bias), e(state0)
+    kda_short_conv_bwd(x, w, bias, state0, dy, dstate_T, dx, dw, dbias, dstate0, workspace, cu_seqlens=cu_seqlens,
+                       silu=silu, zero_rest=cu_seqlens is not None, stream=stream)
+    return dx, dw, dbias, dstate0
+
+
+def short_conv_step(x, w, bias, state, *, state_out=None, silu=True, y=None, stream=None):
+    """One row a sequence; state is updated in place unless state_out is given.  Returns y."""
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    kda_short_conv_step(x, w, bias, state, state if state_out is None else state_out, y, silu=silu, stream=stream)
+    return y
+
+
+# ------------------------------------------------------------------ selective scan
+def _ssm_call(u, A, Bm, cu_seqlens, dt_softplus, zero_rest, step=False):
+    for t, name in ((u, "u"), (A, "A"), (Bm, "Bm")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    if A.dim() != 2:
+        raise ValueError(f"A has shape {tuple(A.shape)}, expected [D, N]")
+    if step:
+        if u.dim() != 2:
+            raise ValueError(f"u has shape {tuple(u.shape)}, expected [B, D]")
+        lead, B, T = u.shape[:1], u.shape[0], 1
+    else:
+        lead, B, T = _sequences(u, cu_seqlens)
+    if Bm.dim() != len(lead) + 2:
+        raise ValueError(f"Bm has shape {tuple(Bm.shape)}, expected {tuple(lead)} + [G, N]")
+    call = _Call(u, "u", lead)
+    D, N, G = u.shape[-1], A.shape[1], Bm.shape[-2]
+    _sizes(B, T, D, N, G)
+    d = kda_ssm_dims(B=B, T=T, D=D, N=N, G=G, dt_softplus=bool(dt_softplus), cu_seqlens=_cu(call, cu_seqlens),
+                     zero_rest=bool(zero_rest))
+    return call, d, (B, D, N)
+
+
+def _ssm_inputs(call, d, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, state):
+    pu, d.ld_u = call.rows(u, "u", (d.D,))
+    pdt, d.ld_dt = call.rows(dt, "dt", (d.D,))
+    pz, d.ld_z = call.rows(z, "z", (d.D,))
+    pB, d.ld_B = call.rows(Bm, "Bm", (d.G, d.N))
+    pC, d.ld_C = call.rows(Cm, "Cm", (d.G, d.N))
+    return (pu, pdt, call.flat(A, "A", (d.D, d.N), _F32), pB, pC, call.flat(Dskip, "Dskip", (d.D,), _F32), pz,
+            call.flat(dt_bias, "dt_bias", (d.D,), _F32), call.flat(h0, "h0", state, _F32))
+
+
+def kda_ssm_scan_fwd_workspace_bytes(u, A, Bm, *, cu_seqlens=None) -> int:
+    """Workspace bytes ``kda_ssm_scan_fwd`` needs for these tensors."""
+    _, d, _ = _ssm_call(u, A, Bm, cu_seqlens, True, False)
+    return int(_lib.kda_ssm_scan_fwd_workspace_bytes(d, _opts(u.dtype)))
+
+
+def kda_ssm_scan_fwd(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, out, h_T, workspace, *, cu_seqlens=None,
+                     dt_softplus=True, zero_rest=False, stream=None) -> None:
+    """Call ``kda_ssm_scan_fwd``; u, dt, z, out [B,T,D] or packed [rows,D], A [D,N], Bm, Cm [...,G,N]."""
+    call, d, state = _ssm_call(u, A, Bm, cu_seqlens, dt_softplus, zero_rest)
+    args = _ssm_inputs(call, d, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, state)
+    po, d.ld_out = call.rows(out, "out", (d.D,))
+    _launch(_lib.kda_ssm_scan_fwd, call, args + (po, call.flat(h_T, "h_T", state, _F32)), d,
+            _opts(u.dtype, workspace, call.device), stream)
+
+
+def kda_ssm_scan_bwd_workspace_bytes(u, A, Bm, *, cu_seqlens=None) -> int:
+    """Workspace bytes ``kda_ssm_scan_bwd`` needs for these tensors."""
+    _, d, _ = _ssm_call(u, A, Bm, cu_seqlens, True, False)
+    return int(_lib.kda_ssm_scan_bwd_workspace_bytes(d, _opts(u.dtype)))
+
+
+def kda_ssm_scan_bwd(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, dout, dh_T, du, ddt, dA, dB, dC, dDskip, dz, ddt_bias,
+                     dh0, workspace, *, cu_seqlens=None, dt_softplus=True, zero_rest=False, stream=None) -> None:
+    """Call ``kda_ssm_scan_bwd``: gradients of <dout, out> + <dh_T, h_T> of ``kda_ssm_scan_fwd``."""
+    call, d, state = _ssm_call(u, A, Bm, cu_seqlens, dt_softplus, zero_rest)
+    args = _ssm_inputs(call, d, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, state)
+    po, d.ld_out = call.rows(dout, "dout", (d.D,))
+    row, bc = call.lead + (d.D,), call.lead + (d.G, d.N)
+    args += (po, call.flat(dh_T, "dh_T", state, _F32), call.flat(du, "du", row), call.flat(ddt, "ddt", row),
+             call.flat(dA, "dA", (d.D, d.N), _F32), call.flat(dB, "dB", bc), call.flat(dC, "dC", bc),
+             call.flat(dDskip, "dDskip", (d.D,), _F32), call.flat(dz, "dz", row),
+             call.flat(ddt_bias, "ddt_bias", (d.D,), _F32), call.flat(dh0, "dh0", state, _F32))
+    _launch(_lib.kda_ssm_scan_bwd, call, args, d, _opts(u.dtype, workspace, call.device), stream)
+
+
+def kda_ssm_step(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h, h_out, out, *, dt_softplus=True, stream=None) -> None:
+    """Call ``kda_ssm_step``; u, dt, z, out [B,D], Bm, Cm [B,G,N], h, h_out [B,D,N] (h_out may be h)."""
+    call, d, state = _ssm_call(u, A, Bm, None, dt_softplus, False, step=True)
+    args = _ssm_inputs(call, d, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h, state)
+    po, d.ld_out = call.rows(out, "out", (d.D,))
+    _launch(_lib.kda_ssm_step, call, args + (call.flat(h_out, "h_out", state, _F32), po), d, _opts(u.dtype), stream)
+
+
+def ssm_scan_fwd(u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, h0=None, *, cu_seqlens=None, dt_softplus=True,
+                 out=None, workspace=None, stream=None):
+    """Selective scan over sequences; returns (out, h_T)."""
+    if workspace is None:
+        workspace = _workspace(kda_ssm_scan_fwd_workspace_bytes(u, A, Bm, cu_seqlens=cu_seqlens), u.device, stream)
+    zero = out is None and cu_seqlens is not None
+    if out is None:
+        out = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+    B = u.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    h_T = torch.empty((B,) + A.shape, dtype=_F32, device=u.device)
+    kda_ssm_scan_fwd(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, out, h_T, workspace, cu_seqlens=cu_seqlens,
+                     dt_softplus=dt_softplus, zero_rest=zero, stream=stream)
+    return out, h_T
+
+
+def ssm_scan_bwd(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, dout, dh_T=None, *, cu_seqlens=None, dt_softplus=True,
+                 workspace=None, stream=None):
+    """Gradients of ``ssm_scan_fwd``; returns (du, ddt, dA, dB, dC, dDskip, dz, ddt_bias, dh0), None for
+    what was not passed."""
+    if workspace is None:
+        workspace = _workspace(kda_ssm_scan_bwd_workspace_bytes(u, A, Bm, cu_seqlens=cu_seqlens), u.device, stream)
+    e = lambda t, dtype: None if t is None else torch.empty(t.shape, dtype=dtype, device=u.device)  # noqa: E731
+    g = (e(u, u.dtype), e(u, u.dtype), e(A, _F32), e(Bm, u.dtype), e(Bm, u.dtype), e(Dskip, _F32), e(z, u.dtype),
+         e(dt_bias, _F32), e(h0, _F32))
+    kda_ssm_scan_bwd(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, dout, dh_T, *g, workspace, cu_seqlens=cu_seqlens,
+                     dt_softplus=dt_softplus, zero_rest=cu_seqlens is not None, stream=stream)
+    return g
+
+
+def ssm_step(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h, *, h_out=None, dt_softplus=True, out=None, stream=None):
+    """One token a sequence; h is updated in place unless h_out is given.  Returns out."""
+    if out is None:
+        out = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+    kda_ssm_step(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h, h if h_out is None else h_out, out,
+                 dt_softplus=dt_softplus, stream=stream)
+    return out
+
+
+# ------------------------------------------------------------------ block norm
+def _norm_call(residual, name, eps):
+    if not isinstance(residual, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if residual.dim() < 1:
+        raise ValueError(f"{name} must be [..., D]")
+    lead, D = residual.shape[:-1], residual.shape[-1]
+    rows = math.prod(lead)
+    _sizes(rows, D)
+    return _Call(residual, name, lead), kda_norm_dims(rows=rows, D=D, eps=eps)
+
+
+def kda_block_norm_fwd(residual, block, gate, scale, w_post, w_pre, res_out, x, *, eps=1e-5, stream=None) -> None:
+    """Call ``kda_block_norm_fwd``; residual, block, gate, res_out, x [..., D]; scale, w_post, w_pre [D]."""
+    call, d = _norm_call(residual, "residual", eps)
+    w, row = (d.D,), residual.shape
+    pr, d.ld_res = call.rows(residual, "residual", w)
+    pb, d.ld_block = call.rows(block, "block", w)
+    pg, d.ld_gate = call.rows(gate, "gate", w)
+    args = (pr, pb, pg, call.flat(scale, "scale", w, _F32), call.flat(w_post, "w_post", w, _F32),
+            call.flat(w_pre, "w_pre", w, _F32), call.flat(res_out, "res_out", row), call.flat(x, "x", row))
+    _launch(_lib.kda_block_norm_fwd, call, args, d, _opts(residual.dtype), stream)
+
+
+def kda_block_norm_bwd_workspace_bytes(res_out) -> int:
+    """Workspace bytes ``kda_block_norm_bwd`` needs for these rows."""
+    _, d = _norm_call(res_out, "res_out", 0.0)
+    return int(_lib.kda_block_norm_bwd_workspace_bytes(d, _opts(res_out.dtype)))
+
+
+def kda_block_norm_bwd(res_out, block, gate, scale, w_post, w_pre, dres, dx, dresidual, dblock, dgate, dscale,
+                       dw_post, dw_pre, workspace, *, eps=1e-5, stream=None) -> None:
+    """Call ``kda_block_norm_bwd``: gradients of <dres, res_out> + <dx, x> of ``kda_block_norm_fwd``."""
+    call, d = _norm_call(res_out, "res_out", eps)
+    w, row = (d.D,), res_out.shape
+    pr, d.ld_res = call.rows(res_out, "res_out", w)
+    pb, d.ld_block = call.rows(block, "block", w)
+    pg, d.ld_gate = call.rows(gate, "gate", w)
+    args = (pr, pb, pg, call.flat(scale, "scale", w, _F32), call.flat(w_post, "w_post", w, _F32),
+            call.flat(w_pre, "w_pre", w, _F32), call.flat(dres, "dres", row), call.flat(dx, "dx", row),
+            call.flat(dresidual, "dresidual", row), call.flat(dblock, "dblock", row), call.flat(dgate, "dgate", row),
+            call.flat(dscale, "dscale", w, _F32), call.flat(dw_post, "dw_post", w, _F32),
+            call.flat(dw_pre, "dw_pre", w, _F32))
+    _launch(_lib.kda_block_norm_bwd, call, args, d, _opts(res_out.dtype, workspace, call.device), stream)
+
+
+def block_norm_fwd(residual, block=None, gate=None, scale=None, w_post=None, w_pre=None, *, eps=1e-5,
+                   want_x=True, stream=None):
+    """Norms behind a block and ahead of the next; returns (res_out, x), None for what is not computed."""
+    e = lambda want: torch.empty(residual.shape, dtype=residual.dtype, device=residual.device) if want else None  # noqa: E731
+    res_out, x = e(block is not None), e(want_x)
+    kda_block_norm_fwd(residual, block, gate, scale, w_post, w_pre, res_out, x, eps=eps, stream=stream)
+    return res_out, x
+
+
+def block_norm_bwd(res_out, block, gate, scale, w_post, w_pre, dres, dx, *, eps=1e-5, workspace=None, stream=None):
+    """Gradients of ``block_norm_fwd``; returns (dresidual, dblock, dgate, dscale, dw_post, dw_pre), None for
+    what was not passed."""
+    if workspace is None:
+        workspace = _workspace(kda_block_norm_bwd_workspace_bytes(res_out), res_out.device, stream)
+    e = lambda t, dtype: None if t is None else torch.empty(t.shape, dtype=dtype, device=res_out.device)  # noqa: E731
+    g = (e(res_out, res_out.dtype), e(block, res_out.dtype), e(gate, res_out.dtype), e(scale, _F32), e(w_post, _F32),
+         e(w_pre, _F32))
+    kda_block_norm_bwd(res_out, block, gate, scale, w_post, w_pre, dres, dx, *g, workspace, eps=eps, stream=stream)
+    return g
