@@ -15,6 +15,7 @@ using namespace kda;
 namespace {
 
 constexpr long long kMaxElems = 1LL << 40;   // refuse sizes whose byte offsets could overflow
+constexpr long long kMaxStride = 1LL << 27;  // a few rows' offsets fit 32 bits of bytes
 
 kda_opts resolve(const kda_opts *o) {
     kda_opts r;
@@ -59,7 +60,7 @@ bool distinct(std::initializer_list<const void *> outs, std::initializer_list<co
 int stride(long long &ld, long long length) {
     if (ld == 0) ld = length;
     if (ld < 0) return KDA_ERR_ARG;
-    return ld < length || ld > kMaxElems ? KDA_ERR_SHAPE : KDA_OK;
+    return ld < length || ld > kMaxStride ? KDA_ERR_SHAPE : KDA_OK;
 }
 int check_rows(int B, int T, bool packed, long long widest, long long *rows) {
     if (B < 0 || T < 0) return KDA_ERR_ARG;

@@ -6,28 +6,95 @@
 namespace kda {
 
 // ---------------------------------------------------------------- V consecutive values
-// V * sizeof(T) is 2, 4, 8, 16 or 32 bytes; the address is a multiple of min(that, 16).
+// V * sizeof(T) is 2, 4, 8, 16, 32 or 64 bytes; a whole access wants the address to be a multiple
+// of min(that, 16).  Values stay in the words that were loaded until widen(): a value taken out of
+// its word earlier, where two ways of loading meet, would make the thread wait for the load there.
 template <typename T, int V>
-struct alignas(V * sizeof(T) < 16 ? V * sizeof(T) : 16) Raw {
-    T v[V];
+struct Raw {
+    static constexpr int kBytes = V * (int)sizeof(T);
+    static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
+    uint32_t w[kWords];
 };
 
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> load_raw(const T *p) {
-    return *reinterpret_cast<const Raw<T, V> *>(p);
+    using R = Raw<T, V>;
+    R r;
+    if constexpr (R::kBytes == 2) {
+        r.w[0] = *reinterpret_cast<const unsigned short *>(p);
+    } else if constexpr (R::kBytes == 4) {
+        r.w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (R::kBytes == 8) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        r.w[0] = v.x;
+        r.w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < R::kWords; i += 4) {
+            const uint4 v = reinterpret_cast<const uint4 *>(p)[i / 4];
+            r.w[i] = v.x;
+            r.w[i + 1] = v.y;
+            r.w[i + 2] = v.z;
+            r.w[i + 3] = v.w;
+        }
+    }
+    return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_raw(T *p, const Raw<T, V> &r) {
+    using R = Raw<T, V>;
+    if constexpr (R::kBytes == 2) {
+        *reinterpret_cast<unsigned short *>(p) = (unsigned short)r.w[0];
+    } else if constexpr (R::kBytes == 4) {
+        *reinterpret_cast<uint32_t *>(p) = r.w[0];
+    } else if constexpr (R::kBytes == 8) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(r.w[0], r.w[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < R::kWords; i += 4)
+            reinterpret_cast<uint4 *>(p)[i / 4] = make_uint4(r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void widen(const Raw<T, V> &r, float *x) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = __uint_as_float(r.w[i]);
+    } else {   // bf16 is the upper half of FP32
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = __uint_as_float(i & 1 ? r.w[i / 2] & 0xffff0000u : r.w[i / 2] << 16);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> narrow(const float *x) {
+    Raw<T, V> r;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r.w[i] = __float_as_uint(x[i]);
+    } else if constexpr (V == 1) {
+        r.w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(x[0]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[i], x[i + 1]);
+            r.w[i / 2] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    }
+    return r;
 }
 // The first n values (n <= 0: none) one by one; the others are zero.
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> load_part(const T *p, int n) {
     Raw<T, V> r;
 #pragma unroll
-    for (int i = 0; i < V; ++i) r.v[i] = i < n ? p[i] : from_f32<T>(0.f);
-    return r;
-}
-template <typename T, int V>
-__device__ __forceinline__ void widen(const Raw<T, V> &r, float *x) {
+    for (int i = 0; i < Raw<T, V>::kWords; ++i) r.w[i] = 0u;
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = to_f32(r.v[i]);
+    for (int i = 0; i < V; ++i)
+        if (i < n) {
+            if constexpr (sizeof(T) == 4) r.w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+            else r.w[i / 2] |= (uint32_t)reinterpret_cast<const unsigned short *>(p)[i] << (i & 1 ? 16 : 0);
+        }
+    return r;
 }
 template <typename T, int V>
 __device__ __forceinline__ void load_f32(const T *p, float *x) {
@@ -35,10 +102,7 @@ __device__ __forceinline__ void load_f32(const T *p, float *x) {
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_f32(T *p, const float *x) {
-    Raw<T, V> r;
-#pragma unroll
-    for (int i = 0; i < V; ++i) r.v[i] = from_f32<T>(x[i]);
-    *reinterpret_cast<Raw<T, V> *>(p) = r;
+    store_raw<T, V>(p, narrow<T, V>(x));
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_part(T *p, const float *x, int n) {
@@ -66,18 +130,17 @@ __device__ __forceinline__ float rcp(float x) {
 __device__ __forceinline__ float sigmoid_f32(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
 __device__ __forceinline__ float silu_f32(float x) { return x * sigmoid_f32(x); }
 
-// log(1 + e^x) = max(x, 0) + 2 atanh(e / (2 + e)) with e = exp(-|x|) in (0, 1]: the series of
-// atanh in s = e / (2 + e) <= 1/3 keeps the relative precision of small values, which
-// log2(1 + e) loses.  The first term left out, s^14 / 15, is below 2^-25 of the sum.
+// log(1 + e^x) = max(x, 0) + 2 atanh(e / (2 + e)) with e = exp(-|x|) in (0, 1]: atanh in
+// s = e / (2 + e) <= 1/3 keeps the relative precision of small values, which log2(1 + e) loses.
+// atanh(s) / s is a polynomial of degree 4 in s^2 through the Chebyshev points of [0, 1/9]
+// (relative error 2^-27).
 __device__ __forceinline__ float softplus_f32(float x) {
     const float e = ex2(-kLog2e * fabsf(x));
     const float s = e * rcp(2.f + e);
     const float q = s * s;
-    float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-    p = fmaf(q, p, 1.f / 9.f);
-    p = fmaf(q, p, 1.f / 7.f);
-    p = fmaf(q, p, 1.f / 5.f);
-    p = fmaf(q, p, 1.f / 3.f);
+    float p = fmaf(q, 0.14078889f, 0.13982579f);
+    p = fmaf(q, p, 0.20012298f);
+    p = fmaf(q, p, 0.33333161f);
     p = fmaf(q, p, 1.f);
     return fmaf(2.f * s, p, fmaxf(x, 0.f));
 }

@@ -110,6 +110,35 @@ struct BcTile {
     }
 };
 
+// 2^x of two values on the FMA pipe, which has room while the special-function unit (16 results a
+// clock and SM) is what the scans wait for.  x = n + f with f in [-1/2, 1/2]; 2^f = 1 + f p(f), p the
+// polynomial of degree 5 through (2^f - 1) / f at its Chebyshev points: the relative error is 2^-26.7
+// anywhere, and that of 2^f - 1 near 0 is 2^-28, which counts where factors close to 1 are multiplied
+// thousands of times.  2^n is put together from n's bits.  Clamped to 2^-127 = 0 and 2^128 = inf;
+// NaN stays NaN.
+__device__ __forceinline__ float clamp_exponent(float x) {
+    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x));   // -127
+    asm("min.NaN.f32 %0, %0, 0f43000000;" : "+f"(x));   // 128
+    return x;
+}
+__device__ __forceinline__ float2 ex2_poly(float2 x) {
+    constexpr float kRound = 12582912.f;   // 1.5 * 2^23: the sum's low bits are n
+    x = make_float2(clamp_exponent(x.x), clamp_exponent(x.y));
+    const float2 t = __fadd2_rn(x, make_float2(kRound, kRound));
+    const float2 n = __fadd2_rn(t, make_float2(-kRound, -kRound));
+    const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
+    float2 p = make_float2(1.5453163e-4f, 1.5453163e-4f);
+    p = __ffma2_rn(p, f, make_float2(1.3390863e-3f, 1.3390863e-3f));
+    p = __ffma2_rn(p, f, make_float2(9.6180830e-3f, 9.6180830e-3f));
+    p = __ffma2_rn(p, f, make_float2(5.5503570e-2f, 5.5503570e-2f));
+    p = __ffma2_rn(p, f, make_float2(2.4022651e-1f, 2.4022651e-1f));
+    p = __ffma2_rn(p, f, make_float2(6.9314718e-1f, 6.9314718e-1f));
+    p = __ffma2_rn(p, f, make_float2(1.f, 1.f));
+    const float2 s = make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
+                                 __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000));
+    return __fmul2_rn(p, s);
+}
+
 // Fills in sizes and layout; the kernels' own pointers are the launchers' to set.
 template <int N>
 SsmP ssm_params(const SsmArgs &a, int L) {

@@ -3,125 +3,404 @@
 //   delta = softplus(dt + dt_bias),  h_t = exp(delta A) h_{t-1} + delta u B_t,
 //   out = (C_t . h_t + Dskip u) z sigmoid(z)
 //
-// A channel's recurrence is sequential in time, its N states and all channels are independent.
-// The states stay in registers, four a lane; a tile of 16 tokens is loaded by all threads while
-// the one before it is computed, delta and delta u are worked out once a (token, channel) and
-// read from shared memory by the channel's lanes.  One exponential a state and token: the
-// special-function unit takes 16 a clock and SM, which bounds the kernel before HBM does.
+// A channel's recurrence is sequential in time, its N states and all channels are independent;
+// the states stay in registers.  One exponential a state and token: the special-function unit takes
+// 16 a clock and SM (4.5e12 a second on the device), which bounds the scan before HBM does (8192
+// tokens x 4096 channels x 16 states: 119 us of exponentials, 41 us of bytes).  Three ways, chosen by
+// plan() from measured costs:
 //
-// Where sequences and channels alone leave the device idle, time is cut into spans.  A span's
-// effect on the state is h -> exp(A sum delta) h + (its end from zero), so one sweep finds the
-// ends of all spans, a small pass chains them, and the spans then run side by side; that doubles
-// the exponentials.
+//  * whole sequences, a lane a channel (ssm_fwd_kernel): the fewest instructions an update (7.3),
+//    for calls whose channels and sequences fill the device: 200 us for 64 x 128 x 4096 x 16, 75 % of
+//    the special-function unit's rate.
+//  * whole sequences, four states a lane (ssm_seq_kernel): four times the lanes, and warps of their
+//    own for what surrounds the recurrence, so that a few thousand channels fill the device without
+//    a second pass over the exponentials: 307 us for 8192 x 4096 x 16, where the first takes 1780.
+//  * spans of time side by side (ssm_fwd_kernel twice): a span's effect on the state is
+//    h -> exp(A sum delta) h + (its end from zero), so one sweep finds the ends of all spans, a small
+//    pass chains them, and the spans then run side by side, for twice the exponentials: 82 us for
+//    8192 x 256 x 16, where whole sequences take 301 at best.
 #include "kda_ssm.cuh"
 
 namespace kda {
 namespace {
 
+// ---------------------------------------------------------------- a lane a channel
+constexpr int kFwdThreads = 128;
+constexpr int kBatch = 4;       // tokens whose u, dt and z a channel's lanes hold at a time
+
+// A channel's N states lie on NQ neighbouring lanes, SPT (at most 16) a lane.
+template <int N>
+struct FwdShape {
+    static constexpr int SPT = N < 16 ? N : 16;
+    static constexpr int NQ = N / SPT;
+    static constexpr int CH = kFwdThreads / NQ;          // channels a block
+    static constexpr int BATCH = NQ > kBatch ? NQ : kBatch;   // tokens whose u, dt and z a channel's lanes hold
+    static constexpr int OWN = BATCH / NQ;               // of them, a lane's: q, q + NQ, ...
+    static constexpr int BC = N / 4;                     // values of B and C a thread loads: 8 threads a token
+};
+
 template <typename T, int N, bool SWEEP>
-__global__ void __launch_bounds__(kSsmThreads) ssm_fwd_kernel(const SsmP a) {
-    using S = SsmShape<N>;
-    constexpr int NQ = S::NQ, CH = S::CH, EPT = S::EPT, ROW = S::ROW;
-    __shared__ __align__(16) float2 sX[kTile * CH];   // delta, delta u
-    __shared__ __align__(16) float sB[kTile * N], sC[kTile * N];
-    __shared__ float sY[kTile * ROW];
+__global__ void __launch_bounds__(kFwdThreads, 4) ssm_fwd_kernel(const SsmP a) {
+    using S = FwdShape<N>;
+    constexpr int SPT = S::SPT, NQ = S::NQ, CH = S::CH, BATCH = S::BATCH, OWN = S::OWN, BC = S::BC, P = SPT / 2;
+    __shared__ __align__(16) float sBC[2][kTile][2 * N];
     const SsmBlock b = ssm_block(a, CH);
     if (b.sp.seq < 0 || (SWEEP && b.sp.k == b.sp.count - 1)) return;
-    const int tid = threadIdx.x;
-    // the recurrence's lanes
-    const int ch = tid / NQ, q = tid % NQ;
+    const int tid = threadIdx.x, ch = tid / NQ, q = tid % NQ, n = b.sp.n;
     const bool live = b.cin + ch < a.Dg;
-    const long long c = (long long)b.g * a.Dg + b.cin + ch;
-    float A2[4] = {0.f, 0.f, 0.f, 0.f}, h[4] = {0.f, 0.f, 0.f, 0.f};
-    if (live) {
-        load_f32<float, 4>(a.A + c * N + 4 * q, A2);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) A2[i] *= kLog2e;
-        if (!SWEEP) {
-            const float *src = b.sp.k ? a.hst + (b.slot * a.D + c) * N
-                               : a.h0 ? a.h0 + ((long long)b.sp.seq * a.D + c) * N
+    // lanes behind the last channel compute the first one's values again and store nothing
+    const int c = b.g * a.Dg + b.cin + (live ? ch : 0);
+    float2 A2[P], h[P];
+    {
+        const float *src = SWEEP      ? nullptr
+                           : b.sp.k   ? a.hst + (b.slot * a.D + c) * N
+                           : a.h0     ? a.h0 + ((long long)b.sp.seq * a.D + c) * N
                                       : nullptr;
-            if (src) load_f32<float, 4>(src + 4 * q, h);
+#pragma unroll
+        for (int i = 0; i < P; i += 2) {
+            const float4 v = *reinterpret_cast<const float4 *>(a.A + (long long)c * N + q * SPT + 2 * i);
+            A2[i] = make_float2(v.x * kLog2e, v.y * kLog2e);
+            A2[i + 1] = make_float2(v.z * kLog2e, v.w * kLog2e);
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (src) s = *reinterpret_cast<const float4 *>(src + q * SPT + 2 * i);
+            h[i] = make_float2(s.x, s.y);
+            h[i + 1] = make_float2(s.z, s.w);
         }
     }
-    // the tile's loads
-    const int lt = tid >> 4, lc = (tid & 15) * EPT;
-    const int lleft = a.Dg - b.cin - lc;               // channels of the group from this thread's on
-    const int gc = b.g * a.Dg + b.cin + lc;
-    float bias[EPT], skip[EPT];
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-        bias[i] = a.dt_bias && i < lleft ? a.dt_bias[gc + i] : 0.f;
-        skip[i] = a.Dskip && i < lleft ? a.Dskip[gc + i] : 0.f;
-    }
-    Raw<T, EPT> nu, ndt, nz;
-    BcTile<T, N> bc;
-    auto fetch = [&](int t0) {
-        const int n = b.sp.n - t0;
-        const long long row = b.sp.r0 + t0 + lt;
-        const bool ok = lt < n;
-        nu = load_tile<T, EPT>(a.u, row, a.ld_u, gc, lleft, ok, a.vec);
-        ndt = load_tile<T, EPT>(a.dt, row, a.ld_dt, gc, lleft, ok, a.vec);
-        if (!SWEEP && a.z) nz = load_tile<T, EPT>(a.z, row, a.ld_z, gc, lleft, ok, a.vec);
-        bc.fetch(a, b.sp.r0 + t0, n, b.g, !SWEEP);
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.Dskip ? a.Dskip[c] : 0.f;
+    // B and C of the next tile, a token to eight threads
+    const int bt = tid >> 3, bk = (tid & 7) * BC;
+    const T *pbc = bk < N ? (const T *)a.Bm + (b.sp.r0 + bt) * a.ld_B + b.g * N + bk
+                          : (const T *)a.Cm + (b.sp.r0 + bt) * a.ld_C + b.g * N + bk - N;
+    const long long ldbc = bk < N ? a.ld_B : a.ld_C;
+    auto fetch_bc = [&](int t0) {
+        const bool ok = t0 + bt < n;
+        const T *p = pbc + t0 * ldbc;
+        return ok && a.vecb ? load_raw<T, BC>(p) : load_part<T, BC>(p, ok ? BC : 0);
     };
-    float dsum = 0.f;
-    fetch(0);
-    for (int t0 = 0; t0 < b.sp.n; t0 += kTile) {
-        const bool ok = t0 + lt < b.sp.n;
-        const Raw<T, EPT> zr = nz;
-        float u[EPT], d[EPT];
-        widen<T, EPT>(nu, u);
-        widen<T, EPT>(ndt, d);
+    auto put_bc = [&](const Raw<T, BC> &r, int buf) {
+        float v[BC];
+        widen<T, BC>(r, v);
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-            d[i] += bias[i];
-            if (a.softplus) d[i] = softplus_f32(d[i]);
-            if (!ok || i >= lleft) d[i] = 0.f;   // a row behind the span leaves the state as it is
-            sX[lt * CH + lc + i] = make_float2(d[i], d[i] * u[i]);
-        }
-        bc.put(sB, SWEEP ? nullptr : sC);
-        if (t0 + kTile < b.sp.n) fetch(t0 + kTile);
-        __syncthreads();
+        for (int i = 0; i < BC; ++i) sBC[buf][bt][bk + i] = v[i];
+    };
+    // The lane's own tokens of a batch.  A lane's offset is 32 bits wide and fixed, the rows' base is
+    // the same for all lanes.
+    const unsigned ou = (unsigned)(q * a.ld_u + c), od = (unsigned)(q * a.ld_dt + c), oz = (unsigned)(q * a.ld_z + c),
+                   oo = (unsigned)(q * a.ld_out + c);
+    const T *pu = (const T *)a.u + b.sp.r0 * a.ld_u, *pd = (const T *)a.dt + b.sp.r0 * a.ld_dt;
+    const T *pz = (const T *)a.z + b.sp.r0 * a.ld_z;
+    T *po = (T *)a.out + b.sp.r0 * a.ld_out;
+    const bool gate = !SWEEP && a.z;
+    T nu[OWN], nd[OWN], nz[OWN];
+    auto fetch = [&](int left) {   // the batch at pu, pd, pz, of which `left` tokens are the span's
+        if (left >= BATCH) {
 #pragma unroll
-        for (int tg = 0; tg < kTile; tg += NQ) {
-            float y[NQ];
+            for (int l = 0; l < OWN; ++l) {
+                nu[l] = (pu + l * NQ * a.ld_u)[ou];
+                nd[l] = (pd + l * NQ * a.ld_dt)[od];
+                if (gate) nz[l] = (pz + l * NQ * a.ld_z)[oz];
+            }
+        } else {
 #pragma unroll
-            for (int j = 0; j < NQ; ++j) {
-                const float2 x = sX[(tg + j) * CH + ch];
-                const float4 bv = *reinterpret_cast<const float4 *>(sB + (tg + j) * N + 4 * q);
-                const float bb[4] = {bv.x, bv.y, bv.z, bv.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) h[i] = fmaf(ex2(x.x * A2[i]), h[i], x.y * bb[i]);
-                if (SWEEP) {
-                    dsum += x.x;
-                } else {
-                    const float4 cv = *reinterpret_cast<const float4 *>(sC + (tg + j) * N + 4 * q);
-                    y[j] = fmaf(cv.x, h[0], cv.y * h[1]) + fmaf(cv.z, h[2], cv.w * h[3]);
+            for (int l = 0; l < OWN; ++l) {
+                nu[l] = nd[l] = nz[l] = from_f32<T>(0.f);
+                if (l * NQ + q < left) {
+                    nu[l] = (pu + l * NQ * a.ld_u)[ou];
+                    nd[l] = (pd + l * NQ * a.ld_dt)[od];
+                    if (gate) nz[l] = (pz + l * NQ * a.ld_z)[oz];
                 }
             }
-            if (!SWEEP) sY[(tg + q) * ROW + ch] = reduce_states<NQ>(y, q);
         }
-        __syncthreads();
-        if (!SWEEP && ok) {
-            float y[EPT], z[EPT];
-            if (a.z) widen<T, EPT>(zr, z);
+    };
+    float dsum = 0.f;
+    put_bc(fetch_bc(0), 0);
+    fetch(n);
+    for (int t0 = 0, buf = 0; t0 < n; t0 += kTile, buf ^= 1) {
+        __syncthreads();   // this tile's B and C are there; the other buffer is read no more
+        Raw<T, BC> rbc;
+        if (t0 + kTile < n) rbc = fetch_bc(t0 + kTile);
+#pragma unroll 1
+        for (int b0 = 0; b0 < kTile; b0 += BATCH) {
+            const int left = n - t0 - b0;
+            if (left <= 0) break;
+            float u[OWN], d[OWN], z[OWN], y[BATCH];
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) {
-                y[i] = fmaf(skip[i], u[i], sY[lt * ROW + lc + i]);
-                if (a.z) y[i] *= silu_f32(z[i]);
+            for (int l = 0; l < OWN; ++l) {
+                u[l] = to_f32(nu[l]);
+                if (gate) z[l] = to_f32(nz[l]);
+                d[l] = to_f32(nd[l]) + bias;
+                if (a.softplus) d[l] = softplus_f32(d[l]);
             }
-            T *o = (T *)a.out + (b.sp.r0 + t0 + lt) * a.ld_out + gc;
-            if (a.vec && lleft >= EPT) store_f32<T, EPT>(o, y);
-            else store_part<T, EPT>(o, y, lleft);
+            if (left < BATCH)   // a token behind the span leaves the state as it is
+#pragma unroll
+                for (int l = 0; l < OWN; ++l)
+                    if (l * NQ + q >= left) d[l] = 0.f;
+            pu += BATCH * a.ld_u;
+            pd += BATCH * a.ld_dt;
+            pz += BATCH * a.ld_z;
+            fetch(left - BATCH);
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                float dl = d[i / NQ], x = dl * u[i / NQ];
+                if (NQ > 1) {
+                    dl = __shfl_sync(0xffffffffu, dl, i % NQ, NQ);
+                    x = __shfl_sync(0xffffffffu, x, i % NQ, NQ);
+                }
+                const float *B = sBC[buf][b0 + i] + q * SPT, *C = B + N;
+                const float2 d2 = make_float2(dl, dl), x2 = make_float2(x, x);
+                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+                if (SWEEP) dsum += dl;
+#pragma unroll
+                for (int k = 0; k < P; k += 2) {
+                    const float4 bv = *reinterpret_cast<const float4 *>(B + 2 * k);
+                    float2 e0 = __fmul2_rn(d2, A2[k]), e1 = __fmul2_rn(d2, A2[k + 1]);
+                    // two of 16 exponentials go to the FMA pipe: 2 % faster than none, and than four
+                    e0 = k == 0 ? ex2_poly(e0) : make_float2(ex2(e0.x), ex2(e0.y));
+                    e1 = make_float2(ex2(e1.x), ex2(e1.y));
+                    h[k] = __ffma2_rn(e0, h[k], __fmul2_rn(x2, make_float2(bv.x, bv.y)));
+                    h[k + 1] = __ffma2_rn(e1, h[k + 1], __fmul2_rn(x2, make_float2(bv.z, bv.w)));
+                    if (!SWEEP) {
+                        const float4 cv = *reinterpret_cast<const float4 *>(C + 2 * k);
+                        s0 = __ffma2_rn(make_float2(cv.x, cv.y), h[k], s0);
+                        s1 = __ffma2_rn(make_float2(cv.z, cv.w), h[k + 1], s1);
+                    }
+                }
+                s0 = __fadd2_rn(s0, s1);
+                y[i] = s0.x + s0.y;
+            }
+            if (!SWEEP) {
+#pragma unroll
+                for (int l = 0; l < OWN; ++l) {
+                    float v[NQ];
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) v[j] = y[l * NQ + j];
+                    float o = fmaf(skip, u[l], reduce_states<NQ>(v, q));
+                    if (gate) o *= silu_f32(z[l]);
+                    if (live && l * NQ + q < left) (po + l * NQ * a.ld_out)[oo] = from_f32<T>(o);
+                }
+                po += BATCH * a.ld_out;
+            }
         }
+        if (t0 + kTile < n) put_bc(rbc, buf ^ 1);
     }
     if (!live) return;
-    if (SWEEP) {
-        store_f32<float, 4>(a.hst + (b.slot * a.D + c) * N + 4 * q, h);
-        if (q == 0) a.sdel[b.slot * a.D + c] = dsum;
-    } else if (a.h_T && b.sp.k == b.sp.count - 1) {
-        store_f32<float, 4>(a.h_T + ((long long)b.sp.seq * a.D + c) * N + 4 * q, h);
+    float *dst = SWEEP ? a.hst + (b.slot * a.D + c) * N
+                 : a.h_T && b.sp.k == b.sp.count - 1 ? a.h_T + ((long long)b.sp.seq * a.D + c) * N : nullptr;
+    if (dst)
+#pragma unroll
+        for (int i = 0; i < P; i += 2)
+            *reinterpret_cast<float4 *>(dst + q * SPT + 2 * i) = make_float4(h[i].x, h[i].y, h[i + 1].x, h[i + 1].y);
+    if (SWEEP && q == 0) a.sdel[b.slot * a.D + c] = dsum;
+}
+
+// ---------------------------------------------------------------- lanes for states
+// Warps 0-3 run the recurrence, one each a scheduler: N / 4 lanes a channel, four states a lane.  The
+// other eight load the next tile, work out delta and delta u, and turn the last-but-one tile's parts
+// of C . h into outputs; three tiles are on the way.  Nothing but two barriers a tile ties the two
+// kinds together, so that the recurrence's dependent steps run while the others wait for memory.
+// Two blocks fit an SM: one alone takes 38 ns a token (32 channels x 16 states), two 65.
+
+// bar.sync / bar.arrive of all of a block's threads
+template <int THREADS>
+__device__ __forceinline__ void wait_at(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(THREADS) : "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void arrive_at(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(THREADS) : "memory"); }
+
+// Where the 16-byte chunk c of a row of parts lies: eight threads that read chunks 2 or 4 apart
+// find them in different banks.
+__device__ __forceinline__ int spread(int c) { return (c & ~7) | ((c + (c >> 3)) & 7); }
+
+template <typename T, int N>
+struct SeqShape {
+    static constexpr int SPT = 4;                      // states a lane
+    static constexpr int SCAN = 128, HELP = 256, THREADS = SCAN + HELP;   // threads of either kind
+    static constexpr int NL = N / SPT;                 // lanes a channel
+    static constexpr int CH = SCAN / NL;               // channels a block
+    static constexpr int TT = CH >= 64 ? 16 : 32;      // tokens a tile
+    static constexpr int E = TT * CH / HELP > 0 ? TT * CH / HELP : 1;   // (token, channel) places a helper thread has in a tile
+    static constexpr int EV = E < 4 ? E : 4;           // neighbouring channels of them
+    static constexpr int PASS = E / EV;
+    static constexpr int TPR = CH / EV;                // threads a token
+    static constexpr int TSTEP = HELP / TPR;           // tokens between a thread's places
+    static constexpr int VB = TT * 2 * N / HELP;       // values of B and C a helper thread loads
+    static constexpr int BPT = 2 * N / VB;             // threads a token
+    static constexpr int STAGES = 3;
+    struct Stage {
+        float2 x[TT][CH];              // delta, delta u
+        float bc[TT][2 * N];
+        float y[TT][SCAN];             // the lanes' parts of C . h
+        T u[TT][CH], z[TT][CH];
+    };
+};
+
+template <typename T, int N>
+__global__ void __launch_bounds__(SeqShape<T, N>::THREADS, 2) ssm_seq_kernel(const SsmP a) {
+    using S = SeqShape<T, N>;
+    constexpr int SPT = S::SPT, NL = S::NL, CH = S::CH, TT = S::TT, EV = S::EV, PASS = S::PASS, TPR = S::TPR, TSTEP = S::TSTEP, VB = S::VB,
+                  BPT = S::BPT, ST = S::STAGES, ALL = S::THREADS;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    typename S::Stage *stage = reinterpret_cast<typename S::Stage *>(smem_raw);
+    const SsmBlock b = ssm_block(a, CH);
+    if (b.sp.seq < 0) return;
+    const int n = b.sp.n, tiles = (n + TT - 1) / TT;
+    const int FULL = 1, DONE = 1 + ST;
+    if (threadIdx.x < S::SCAN) {
+        const int tid = threadIdx.x, ch = tid / NL, q = tid % NL;
+        const bool live = b.cin + ch < a.Dg;
+        const long long c = (long long)b.g * a.Dg + b.cin + (live ? ch : 0);
+        const int at_y = spread(tid >> 2) * 4 + (tid & 3);
+        float A2[SPT], h[SPT];
+        load_f32<float, SPT>(a.A + c * N + q * SPT, A2);
+        const float *src = a.h0 ? a.h0 + ((long long)b.sp.seq * a.D + c) * N : nullptr;
+#pragma unroll
+        for (int i = 0; i < SPT; ++i) {
+            A2[i] *= kLog2e;
+            h[i] = 0.f;
+        }
+        if (src) load_f32<float, SPT>(src + q * SPT, h);
+        for (int i = 0; i < tiles; ++i) {
+            typename S::Stage &s = stage[i % ST];
+            wait_at<ALL>(FULL + i % ST);
+            // Four tokens at a time: their decay factors and inputs are worked out while the four
+            // before them go through the recurrence, so that its dependent steps and the exponentials'
+            // latency overlap.
+            float e[4][SPT], in[4][SPT];
+            auto ahead = [&](int j, int t) {
+                const float2 x = s.x[t][ch];
+                float bv[SPT];
+                load_f32<float, SPT>(&s.bc[t][q * SPT], bv);
+#pragma unroll
+                for (int k = 0; k < SPT; k += 2) {
+                    const float2 m = __fmul2_rn(make_float2(x.x, x.x), make_float2(A2[k], A2[k + 1]));
+                    const float2 r = __fmul2_rn(make_float2(x.y, x.y), make_float2(bv[k], bv[k + 1]));
+                    e[j][k] = ex2(m.x);
+                    e[j][k + 1] = ex2(m.y);
+                    in[j][k] = r.x;
+                    in[j][k + 1] = r.y;
+                }
+            };
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ahead(j, j);
+#pragma unroll
+            for (int t = 0; t < TT; t += 4) {
+                float y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float cv[SPT];
+                    load_f32<float, SPT>(&s.bc[t + j][N + q * SPT], cv);
+                    float2 sum;
+#pragma unroll
+                    for (int k = 0; k < SPT; k += 2) {
+                        const float2 hk = __ffma2_rn(make_float2(e[j][k], e[j][k + 1]), make_float2(h[k], h[k + 1]),
+                                                     make_float2(in[j][k], in[j][k + 1]));
+                        h[k] = hk.x;
+                        h[k + 1] = hk.y;
+                        sum = k ? __ffma2_rn(make_float2(cv[k], cv[k + 1]), hk, sum) : __fmul2_rn(make_float2(cv[0], cv[1]), hk);
+                    }
+                    y[j] = sum.x + sum.y;
+                    if (t + 4 < TT) ahead(j, t + 4 + j);
+                }
+                // behind the loads ahead, which could not pass them
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s.y[t + j][at_y] = y[j];
+            }
+            arrive_at<ALL>(DONE + i % ST);
+        }
+        if (!live) return;
+        if (a.h_T) store_f32<float, SPT>(a.h_T + ((long long)b.sp.seq * a.D + c) * N + q * SPT, h);
+        return;
+    }
+    // helpers
+    const int tid = threadIdx.x - S::SCAN;
+    const int lt = tid / TPR, lc = tid % TPR * EV;
+    const int left = a.Dg - b.cin - lc;                       // channels of the group from the thread's first on
+    const int c = b.g * a.Dg + b.cin + lc;
+    const bool gate = a.z != nullptr;
+    float bias[EV], skip[EV];
+#pragma unroll
+    for (int k = 0; k < EV; ++k) {
+        bias[k] = a.dt_bias && k < left ? a.dt_bias[c + k] : 0.f;
+        skip[k] = a.Dskip && k < left ? a.Dskip[c + k] : 0.f;
+    }
+    const int bt = tid / BPT, bk = tid % BPT * VB;
+    const bool is_b = bk < N;
+    const T *pbc = is_b ? (const T *)a.Bm + (b.sp.r0 + bt) * a.ld_B + b.g * N + bk
+                        : (const T *)a.Cm + (b.sp.r0 + bt) * a.ld_C + b.g * N + bk - N;
+    const long long ldbc = is_b ? a.ld_B : a.ld_C;
+    Raw<T, EV> nu[PASS], nd[PASS], nz[PASS];
+    Raw<T, VB> nbc;
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int p = 0; p < PASS; ++p) {
+            const int t = t0 + p * TSTEP + lt;
+            const bool ok = t < n && p * TSTEP + lt < TT;
+            nu[p] = load_tile<T, EV>(a.u, b.sp.r0 + t, a.ld_u, c, left, ok, a.vec);
+            nd[p] = load_tile<T, EV>(a.dt, b.sp.r0 + t, a.ld_dt, c, left, ok, a.vec);
+            if (gate) nz[p] = load_tile<T, EV>(a.z, b.sp.r0 + t, a.ld_z, c, left, ok, a.vec);
+        }
+        const bool ok = t0 + bt < n;
+        nbc = ok && a.vecb ? load_raw<T, VB>(pbc + t0 * ldbc) : load_part<T, VB>(pbc + t0 * ldbc, ok ? VB : 0);
+    };
+    fetch(0);
+    for (int i = 0; i < tiles + 2; ++i) {
+        if (i < tiles) {
+            typename S::Stage &s = stage[i % ST];
+            const int t0 = i * TT;
+#pragma unroll
+            for (int p = 0; p < PASS; ++p) {
+                const int t = p * TSTEP + lt;
+                if (t >= TT) break;
+                float u[EV], d[EV], x[2 * EV];
+                widen<T, EV>(nu[p], u);
+                widen<T, EV>(nd[p], d);
+#pragma unroll
+                for (int k = 0; k < EV; ++k) {
+                    d[k] += bias[k];
+                    if (a.softplus) d[k] = softplus_f32(d[k]);
+                    if (t0 + t >= n || k >= left) d[k] = 0.f;   // a token behind the span leaves the state as it is
+                    x[2 * k] = d[k];
+                    x[2 * k + 1] = d[k] * u[k];
+                }
+                store_f32<float, 2 * EV>(&s.x[t][lc].x, x);
+                store_raw<T, EV>(&s.u[t][lc], nu[p]);
+                if (gate) store_raw<T, EV>(&s.z[t][lc], nz[p]);
+            }
+            float v[VB];
+            widen<T, VB>(nbc, v);
+            store_f32<float, VB>(&s.bc[bt][bk], v);
+            if (i + 1 < tiles) fetch(t0 + TT);
+            arrive_at<ALL>(FULL + i % ST);
+        }
+        if (i >= 2) {
+            typename S::Stage &s = stage[(i - 2) % ST];
+            const int t0 = (i - 2) * TT;
+            wait_at<ALL>(DONE + (i - 2) % ST);
+#pragma unroll
+            for (int p = 0; p < PASS; ++p) {
+                const int t = p * TSTEP + lt;
+                if (t >= TT || t0 + t >= n) break;
+                float u[EV], z[EV], y[EV];
+                load_f32<T, EV>(&s.u[t][lc], u);
+                if (gate) load_f32<T, EV>(&s.z[t][lc], z);
+                float part[EV * NL];
+#pragma unroll
+                for (int m = 0; m < EV * NL; m += 4)
+                    load_f32<float, 4>(&s.y[t][spread((lc * NL + m) >> 2) * 4], part + m);
+#pragma unroll
+                for (int k = 0; k < EV; ++k) {
+#pragma unroll
+                    for (int o = NL / 2; o >= 1; o /= 2)
+#pragma unroll
+                        for (int m = 0; m < o; ++m) part[k * NL + m] += part[k * NL + m + o];
+                    y[k] = fmaf(skip[k], u[k], part[k * NL]);
+                    if (gate) y[k] *= silu_f32(z[k]);
+                }
+                T *o = (T *)a.out + (b.sp.r0 + t0 + t) * a.ld_out + c;
+                if (a.vec && left >= EV) store_f32<T, EV>(o, y);
+                else store_part<T, EV>(o, y, left);
+            }
+        }
     }
 }
 
@@ -212,43 +491,82 @@ __global__ void __launch_bounds__(128) ssm_step_kernel(const SsmP a) {
     }
 }
 
-// Rows a span of the forward takes: whole sequences where their blocks give each SM one,
-// otherwise spans for three blocks a SM.  Packed sequences' lengths are not known here: a span
-// holds twice the mean, so that even ones stay whole and a long one among short ones is cut.
-int fwd_span(const SsmArgs &a) {
-    const int CH = 4 * kSsmThreads / a.N, Dg = a.D / a.G;
-    const long long per_span = (long long)a.G * ((Dg + CH - 1) / CH);
-    const long long want = 444 / per_span;   // spans in all
-    const long long longest = a.T > 0 ? a.T : 1;
-    long long L;
-    if (a.cu) {
-        const long long n = want > a.S ? want : a.S;
-        L = n > 1 ? (2 * a.rows + n - 1) / n : longest;
-    } else {
-        if (want <= 1 || per_span * a.S >= 148) return (int)longest;
-        L = (a.rows + want - 1) / want;
+// Which kernel, and the rows a span takes (L >= T: whole sequences).  Estimated nanoseconds, from
+// measurements on a B200 between 256 and 12288 channels, 128 and 8192 tokens, 8 and 64 states:
+//   four states a lane   a token 38 with one block a SM, 65 with two, and so on in pairs
+//   a lane a channel     a token 100 + 105 k, k warps a scheduler (at least one), from four on 68 + 113 k
+//   spans                0.00076 an update and 0.0024 a channel and token, and 20 us for its passes
+// Packed sequences' lengths are not known here: they count as 1.5 times the mean, and a span
+// holds twice the mean of as many rows as spans are wanted, so that even sequences stay whole.
+struct FwdPlan {
+    bool lanes;   // four states a lane
+    int L;
+};
+FwdPlan plan(const SsmArgs &a) {
+    const int Dg = a.D / a.G, ch_seq = 512 / a.N, ch = kFwdThreads / (a.N <= 16 ? 1 : a.N / 16);
+    const long long rows = a.rows, whole = a.T > 0 ? a.T : 1;
+    const double len = a.cu && a.S > 1 ? 1.5 * rows / a.S : (double)a.T;
+    const long long blocks_seq = (long long)a.S * a.G * ((Dg + ch_seq - 1) / ch_seq), per_span = (long long)a.G * ((Dg + ch - 1) / ch);
+    const long long n = (blocks_seq + 147) / 148;
+    const double t_seq = len * (n / 2 * 65.0 + n % 2 * 38.0);
+    const double k = (double)per_span * a.S / 148.0;   // warps a scheduler: blocks of four warps
+    const double t_whole = len * (k <= 4.0 ? 100.0 + 105.0 * (k > 1.0 ? k : 1.0) : 68.0 + 113.0 * k);
+    const double t_span = (double)rows * a.D * (0.00076 * a.N + 0.0024) + 20000.0;
+    if (t_span < t_seq && t_span < t_whole) {
+        const long long want = 592 / per_span > 1 ? 592 / per_span : 1;   // spans in all: one wave of 4 blocks a SM
+        const long long m = want > a.S ? want : a.S;
+        long long L = a.cu ? (2 * rows + m - 1) / m : (rows + want - 1) / want;
+        L = (L + kTile - 1) / kTile * kTile;
+        if (L < 64) L = 64;
+        if (L < whole) return {false, (int)L};
     }
-    L = (L + kTile - 1) / kTile * kTile;
-    if (L < 64) L = 64;
-    return (int)(L < longest ? L : longest);
+    return {t_seq < t_whole, (int)whole};
+}
+
+template <typename T, int N>
+cudaError_t run_seq(const SsmArgs &a, cudaStream_t st) {
+    using S = SeqShape<T, N>;
+    SsmP p = ssm_params<N>(a, a.T > 0 ? (int)a.T : 1);
+    p.cpg = (p.Dg + S::CH - 1) / S::CH;
+    p.nblk = p.cpg * a.G;
+    long long ld = a.ld_u | a.ld_dt | (a.z ? a.ld_z : 0) | a.ld_out | p.Dg;
+    for (const void *r : {a.u, a.dt, a.z, (const void *)a.out}) ld |= elements(r, a.bf16);
+    p.vec = ld % S::EV == 0;
+    constexpr int most = S::VB * sizeof(T) < 16 ? S::VB : 16 / sizeof(T);
+    p.vecb = (a.ld_B | a.ld_C | elements(a.Bm, a.bf16) | elements(a.Cm, a.bf16)) % most == 0;
+    const long long blocks = p.slots * p.nblk;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    constexpr int smem = sizeof(typename S::Stage) * S::STAGES;
+    const cudaError_t e = cudaFuncSetAttribute(ssm_seq_kernel<T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    a.marks->mark(st);
+    ssm_seq_kernel<T, N><<<(unsigned)blocks, S::THREADS, smem, st>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename T, int N>
 cudaError_t run_fwd(const SsmArgs &a, cudaStream_t st) {
-    SsmP p = ssm_params<N>(a, fwd_span(a));
+    const FwdPlan f = plan(a);
+    if (f.lanes) return run_seq<T, N>(a, st);
+    using F = FwdShape<N>;
+    SsmP p = ssm_params<N>(a, f.L);
+    p.cpg = (p.Dg + F::CH - 1) / F::CH;
+    p.nblk = p.cpg * a.G;
+    constexpr int most = F::BC * sizeof(T) < 16 ? F::BC : 16 / sizeof(T);
+    p.vecb = (a.ld_B | a.ld_C | elements(a.Bm, a.bf16) | elements(a.Cm, a.bf16)) % most == 0;
     const long long blocks = p.slots * p.nblk;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (p.L < a.T) {
         p.hst = (float *)a.workspace;
         p.sdel = p.hst + p.slots * a.D * N;
         a.marks->mark(st);
-        ssm_fwd_kernel<T, N, true><<<(unsigned)blocks, kSsmThreads, 0, st>>>(p);
+        ssm_fwd_kernel<T, N, true><<<(unsigned)blocks, kFwdThreads, 0, st>>>(p);
         a.marks->mark(st);
         const cudaError_t e = launch_ssm_seams(p, N, st);
         if (e != cudaSuccess) return e;
     }
     a.marks->mark(st);
-    ssm_fwd_kernel<T, N, false><<<(unsigned)blocks, kSsmThreads, 0, st>>>(p);
+    ssm_fwd_kernel<T, N, false><<<(unsigned)blocks, kFwdThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
 template <typename T, int N>
@@ -280,7 +598,7 @@ cudaError_t launch_ssm_seams(const SsmP &p, int N, cudaStream_t st) {
 }
 
 size_t ssm_scan_fwd_workspace_bytes(const SsmArgs &a) {
-    const int L = fwd_span(a);
+    const int L = plan(a).L;
     if (L >= a.T) return 0;
     return (size_t)span_slots(a.cu != nullptr, a.S, a.T, L) * a.D * (a.N + 1) * sizeof(float);
 }

@@ -18,9 +18,11 @@ import math
 import torch
 
 from . import kda as _kda
-from .kda import KDA_BF16, KDA_F32, KdaError, kda_opts
+from .kda import KDA_F32, KdaError, kda_opts
 
 _lib = _kda._lib
+# what torch.cuda.current_stream(i).cuda_stream and current_device() return, without their objects
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 _ip, _ll, _vp, _sz = ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p, ctypes.c_size_t
 
 
@@ -62,8 +64,10 @@ _F32 = torch.float32
 
 
 # ------------------------------------------------------------------ argument checks
+# A decode step runs for a few microseconds on the device, so a tensor's checks are one chain of
+# cheap comparisons; what is wrong is found out only when something is.
 class _Call:
-    """Checks the tensors of one call: type, shape, device, layout; collects their addresses."""
+    """Checks the tensors of one call: type, shape, device, layout; gives their addresses."""
     __slots__ = ("dtype", "device", "lead")
 
     def __init__(self, x, name, lead):
@@ -71,40 +75,44 @@ class _Call:
             raise TypeError(f"{name} must be a torch.Tensor")
         if not x.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-        self.dtype, self.device, self.lead = x.dtype, x.device, lead
+        self.dtype, self.device, self.lead = x.dtype, x.get_device(), tuple(lead)
 
     def flat(self, t, name, shape, dtype=None):
         """Address of a contiguous tensor of this shape; None stays None."""
         if t is None:
             return None
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != (dtype or self.dtype):
-            raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype or self.dtype}")
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
+        if dtype is None:
+            dtype = self.dtype
+        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == self.device
+                and t.is_contiguous()):
+            return t.data_ptr()
+        self._refuse(t, name, shape, dtype)
+        raise ValueError(f"{name} must be contiguous")
 
     def rows(self, t, name, tail):
         """(address, row stride) of a row tensor [*lead, *tail]; (None, 0) for None."""
         if t is None:
             return None, 0
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != self.dtype:
-            raise TypeError(f"{name} has dtype {t.dtype}, expected {self.dtype}")
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
-        if t.shape != self.lead + tail:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {self.lead + tail}")
+        shape = self.lead + tail
+        if not (isinstance(t, torch.Tensor) and t.dtype is self.dtype and t.shape == shape
+                and t.get_device() == self.device):
+            self._refuse(t, name, shape, self.dtype)
         if t.is_contiguous():
             return t.data_ptr(), 0
-        st, lead = t.stride(), len(self.lead)
-        width = math.prod(tail)
+        return t.data_ptr(), self._row_stride(t.stride(), name, tail)
+
+    def _refuse(self, t, name, shape, dtype):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{self.device}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+    def _row_stride(self, st, name, tail):
+        lead = len(self.lead)
         # the row itself is contiguous
         want = 1
         for n, s in zip(reversed(tail), reversed(st[lead:])):
@@ -123,26 +131,23 @@ class _Call:
                     raise ValueError(f"{name}: rows must be evenly spaced (strides {st})")
             span *= n
         if ld is None:
-            ld = width
-        if ld < width:
+            ld = want
+        if ld < want:
             raise ValueError(f"{name}: rows overlap (strides {st})")
-        return t.data_ptr(), ld
+        return ld
 
 
 def _opts(dtype, workspace=None, device=None):
     o = kda_opts()
-    if dtype == torch.bfloat16:
-        o.dtype = KDA_BF16
-    elif dtype == _F32:
+    if dtype is _F32:
         o.dtype = KDA_F32
-    else:
+    elif dtype is not torch.bfloat16:   # KDA_BF16 is 0
         raise TypeError(f"unsupported activation dtype {dtype}; use bfloat16 or float32")
-    o.scale = 1.0
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor):
             raise TypeError("workspace must be a torch.Tensor")
-        if workspace.device != device:
-            raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+        if workspace.get_device() != device:
+            raise ValueError(f"workspace is on {workspace.device}, expected cuda:{device}")
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         o.workspace = workspace.data_ptr()
@@ -151,17 +156,19 @@ def _opts(dtype, workspace=None, device=None):
 
 
 def _launch(fn, call, args, dims, opts, stream):
-    """Runs the C call on the tensors' device."""
+    """Runs the C call on the tensors' device, whichever is current."""
     dev = call.device
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, expected {dev}")
-    if torch.cuda.current_device() == dev.index:
-        h = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
-        st = fn(*args, dims, opts, h)
+    if stream is None:
+        handle = _raw_stream(dev)
+    else:
+        if stream.device_index != dev:
+            raise ValueError(f"stream is on {stream.device}, expected cuda:{dev}")
+        handle = stream.cuda_stream
+    if _current_device() == dev:
+        st = fn(*args, dims, opts, handle)
     else:
         with torch.cuda.device(dev):
-            h = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
-            st = fn(*args, dims, opts, h)
+            st = fn(*args, dims, opts, handle)
     if st != 0:
         raise KdaError(fn.__name__, st)
 
@@ -176,9 +183,14 @@ def _workspace(nbytes, device, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _sequences(x, cu_seqlens, D_dims=1):
+def _rows_like(x):
+    """A contiguous tensor of x's shape and type."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+def _sequences(x, cu_seqlens):
     """(lead, B, T) of a row tensor; checks cu_seqlens."""
-    lead = x.shape[:-D_dims]
+    lead = tuple(x.shape[:-1])
     if cu_seqlens is None:
         if len(lead) != 2:
             raise ValueError(f"expected [B, T, ...] without cu_seqlens, got shape {tuple(x.shape)}")
@@ -216,7 +228,7 @@ def _conv_call(x, w, cu_seqlens, silu, zero_rest, step=False):
     call = _Call(x, "x", lead)
     D, K = x.shape[-1], w.shape[1]
     _sizes(B, T, D, K)
-    d = kda_conv_dims(B=B, T=T, D=D, K=K, silu=bool(silu), cu_seqlens=_cu(call, cu_seqlens), zero_rest=bool(zero_rest))
+    d = kda_conv_dims(B=B, T=T, D=D, K=K, silu=1 if silu else 0, cu_seqlens=_cu(call, cu_seqlens), zero_rest=1 if zero_rest else 0)
     return call, d, (B, K - 1, D), (D, K)
 
 
@@ -264,7 +276,7 @@ def short_conv_fwd(x, w, bias=None, state0=None, *, cu_seqlens=None, silu=True, 
     """Causal depthwise convolution with SiLU; returns (y, state_T)."""
     zero = y is None and cu_seqlens is not None
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _rows_like(x)
     B = x.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
     state_T = torch.empty((B, w.shape[1] - 1, x.shape[-1]), dtype=x.dtype, device=x.device)
     kda_short_conv_fwd(x, w, bias, state0, y, state_T, cu_seqlens=cu_seqlens, silu=silu, zero_rest=zero, stream=stream)
@@ -286,7 +298,7 @@ def short_conv_bwd(x, w, bias, state0, dy, dstate_T=None, *, cu_seqlens=None, si
 def short_conv_step(x, w, bias, state, *, state_out=None, silu=True, y=None, stream=None):
     """One row a sequence; state is updated in place unless state_out is given.  Returns y."""
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _rows_like(x)
     kda_short_conv_step(x, w, bias, state, state if state_out is None else state_out, y, silu=silu, stream=stream)
     return y
 
@@ -309,8 +321,8 @@ def _ssm_call(u, A, Bm, cu_seqlens, dt_softplus, zero_rest, step=False):
     call = _Call(u, "u", lead)
     D, N, G = u.shape[-1], A.shape[1], Bm.shape[-2]
     _sizes(B, T, D, N, G)
-    d = kda_ssm_dims(B=B, T=T, D=D, N=N, G=G, dt_softplus=bool(dt_softplus), cu_seqlens=_cu(call, cu_seqlens),
-                     zero_rest=bool(zero_rest))
+    d = kda_ssm_dims(B=B, T=T, D=D, N=N, G=G, dt_softplus=1 if dt_softplus else 0, cu_seqlens=_cu(call, cu_seqlens),
+                     zero_rest=1 if zero_rest else 0)
     return call, d, (B, D, N)
 
 
@@ -375,7 +387,7 @@ def ssm_scan_fwd(u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, h0=None, *,
         workspace = _workspace(kda_ssm_scan_fwd_workspace_bytes(u, A, Bm, cu_seqlens=cu_seqlens), u.device, stream)
     zero = out is None and cu_seqlens is not None
     if out is None:
-        out = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+        out = _rows_like(u)
     B = u.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
     h_T = torch.empty((B,) + A.shape, dtype=_F32, device=u.device)
     kda_ssm_scan_fwd(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, out, h_T, workspace, cu_seqlens=cu_seqlens,
@@ -400,7 +412,7 @@ def ssm_scan_bwd(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, dout, dh_T=None, *, cu
 def ssm_step(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h, *, h_out=None, dt_softplus=True, out=None, stream=None):
     """One token a sequence; h is updated in place unless h_out is given.  Returns out."""
     if out is None:
-        out = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+        out = _rows_like(u)
     kda_ssm_step(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h, h if h_out is None else h_out, out,
                  dt_softplus=dt_softplus, stream=stream)
     return out
@@ -455,8 +467,8 @@ def kda_block_norm_bwd(res_out, block, gate, scale, w_post, w_pre, dres, dx, dre
 def block_norm_fwd(residual, block=None, gate=None, scale=None, w_post=None, w_pre=None, *, eps=1e-5,
                    want_x=True, stream=None):
     """Norms behind a block and ahead of the next; returns (res_out, x), None for what is not computed."""
-    e = lambda want: torch.empty(residual.shape, dtype=residual.dtype, device=residual.device) if want else None  # noqa: E731
-    res_out, x = e(block is not None), e(want_x)
+    res_out = _rows_like(residual) if block is not None else None
+    x = _rows_like(residual) if want_x else None
     kda_block_norm_fwd(residual, block, gate, scale, w_post, w_pre, res_out, x, eps=eps, stream=stream)
     return res_out, x
 

@@ -20,7 +20,8 @@
  * none.  Bounds outside 0 .. T are clamped on the device.  Rows of no sequence are neither
  * read nor written, unless zero_rest is set: then the call's row outputs are zero there.
  *
- * Row strides (ld_*) count elements; 0 means the row's own length (contiguous).  A tensor
+ * Row strides (ld_*) count elements; 0 means the row's own length (contiguous); at
+ * most 2^27.  A tensor
  * with a row stride may so be a column range of a wider one, and unlike the others it may
  * start at any element; 16-byte aligned rows are read in wider accesses. Inputs and outputs must not overlap unless a
  * comment says so; where pointers show it, the call is refused (KDA_ERR_ARG).

@@ -22,9 +22,10 @@ def silu(x):
     return x * torch.sigmoid(x)
 
 
-def dsilu(x):
+def dsilu(x, mag=False):
+    """silu' = p + p x (1 - p); its two terms cancel at x = -1.278, so its rounding is relative to their sum."""
     p = torch.sigmoid(x)
-    return p * (1 + x * (1 - p))
+    return p * (1 + (x.abs() if mag else x) * (1 - p))
 
 
 # ------------------------------------------------------------------ short convolution
@@ -120,7 +121,7 @@ def ssm(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, bounds, dout=None, dh_T=None, s
     dA = (kept * delta[..., None]).sum(0)
     fold = lambda v: v.reshape(rows, G, D // G, N).sum(2)  # noqa: E731
     dB, dC = fold(e * (delta * u)[..., None]), fold(h * dy[..., None])
-    dz = None if z is None else dout * y * (dsilu(z).abs() if mag else dsilu(z))
+    dz = None if z is None else dout * y * dsilu(z, mag)
     return du, ddt, dA, dB, dC, (dy * u).sum(0), dz, ddt.sum(0), dh0
 
 

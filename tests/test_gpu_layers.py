@@ -173,6 +173,15 @@ SSM = [
     (_packed([0, 64, 128], 128), 16, 64, 4, False, True, False, True, 8),
     (_packed([0, 0, 0], 3), 16, 16, 1, True, True, True, True, 0),
     (_packed([0], 3), 16, 16, 1, False, True, True, True, 0),
+    # by size: spans of time (few channels, long), four states a lane, a lane a channel
+    (_dense(1, 1500), 8, 8, 1, True, True, True, True, 0),
+    (_packed([0, 700, 701, 1600], 1600), 6, 16, 2, True, True, True, True, 0),
+    (_dense(1, 100), 301, 16, 1, True, True, False, False, 1),
+    (_dense(130, 3), 256, 8, 1, True, True, True, True, 0),
+    (_dense(250, 2), 384, 16, 1, True, True, True, True, 0),
+    (_dense(250, 2), 93, 64, 1, False, True, True, True, 0),
+    (_dense(300, 3), 162, 32, 3, True, False, False, True, 0),
+    (_packed(sorted([0] + [(i * 7919) % 601 for i in range(260)] + [601]), 601), 380, 16, 1, True, True, True, True, 4),
 ] if torch.cuda.is_available() else []
 
 

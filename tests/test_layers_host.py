@@ -152,7 +152,7 @@ def test_binding_refuses_what_the_library_could_not_see(L):
 
 def test_row_strides_of_views(L):
     c = L._Call.__new__(L._Call)
-    c.dtype, c.device = torch.float32, torch.device("cpu")
+    c.dtype, c.device = torch.float32, -1
     t = torch.zeros(3, 5, 12)
     c.lead = (3, 5)
     assert c.rows(t, "t", (12,))[1] == 0
