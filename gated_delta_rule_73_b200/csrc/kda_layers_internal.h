@@ -95,8 +95,4 @@ struct ZeroRest {
 };
 cudaError_t launch_zero_rest(const ZeroRest &z, const int *cu, int S, long long T, cudaStream_t st);
 
-// out[i] = sum over k < count of in[k * stride + i], i < n, in a fixed order.
-cudaError_t launch_sum_rows(const float *in, float *out, long long n, long long count, long long stride,
-                            cudaStream_t st);
-
 }  // namespace kda

@@ -22,31 +22,10 @@ __global__ void __launch_bounds__(256) zero_rest_kernel(const ZeroRest z, const 
     }
 }
 
-__global__ void __launch_bounds__(1024) sum_rows_kernel(const float *__restrict__ in, float *out, long long n,
-                                                        long long count, long long stride) {
-    __shared__ float s[32][33];
-    const long long i = (long long)blockIdx.x * 32 + threadIdx.x;
-    float v = 0.f;
-    if (i < n)
-        for (long long k = threadIdx.y; k < count; k += 32) v += in[k * stride + i];
-    s[threadIdx.y][threadIdx.x] = v;
-    __syncthreads();
-    v = warp_sum(s[threadIdx.x][threadIdx.y]);
-    const long long o = (long long)blockIdx.x * 32 + threadIdx.y;
-    if (threadIdx.x == 0 && o < n) out[o] = v;
-}
-
 }  // namespace
 
 cudaError_t launch_zero_rest(const ZeroRest &z, const int *cu, int S, long long T, cudaStream_t st) {
     zero_rest_kernel<<<T < 296 ? (T > 0 ? (unsigned)T : 1u) : 296u, 256, 0, st>>>(z, cu, S, T);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_sum_rows(const float *in, float *out, long long n, long long count, long long stride,
-                            cudaStream_t st) {
-    if (n <= 0) return cudaSuccess;
-    sum_rows_kernel<<<(unsigned)((n + 31) / 32), dim3(32, 32), 0, st>>>(in, out, n, count, stride);
     return cudaGetLastError();
 }
 

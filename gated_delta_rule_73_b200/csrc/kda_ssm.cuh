@@ -20,23 +20,25 @@ struct SsmP {
     long long ld_u, ld_dt, ld_z, ld_B, ld_C, ld_out, slots;
     // workspace: states and their gradients at the spans' seams [slots][D][N], the spans' sums of
     // delta [slots][D], partial sums (backward)
-    float *hst, *gst, *sdel, *part_A, *part_D, *part_bias, *part_BC;
+    float *hst, *gst, *sdel, *part, *part_BC;   // part: [slots][part_ld], of dA, dDskip, ddt_bias
+    long long part_ld;                          // D N + 2 D up to the next multiple of 4: rows of float4
 };
 
-constexpr int kSsmThreads = 256;
-constexpr int kTile = 16;       // tokens a tile
+constexpr int kTile = 16;       // tokens a tile of B and C
 
-// A channel's N states lie on NQ = N / 4 neighbouring lanes, four a lane; a block holds CH
-// channels.  For the tile's loads 16 threads share a token, EPT channels each.
+// ---------------------------------------------------------------- a lane a channel
+constexpr int kFwdThreads = 128;
+constexpr int kBatch = 4;       // tokens whose u, dt and z a channel's lanes hold at a time
+
+// A channel's N states lie on NQ neighbouring lanes, SPT (at most 16) a lane.
 template <int N>
-struct SsmShape {
-    static constexpr int NQ = N / 4;
-    static constexpr int CH = kSsmThreads / NQ;
-    static constexpr int EPT = CH / 16;
-    static constexpr int BE = N >= 16 ? N / 16 : 1;   // values of B (and of C) a thread loads
-    // a row of CH sums in shared memory: the pad spreads the NQ rows that a warp writes at once
-    // over the banks
-    static constexpr int ROW = CH + 32 / NQ;
+struct FwdShape {
+    static constexpr int SPT = N < 16 ? N : 16;
+    static constexpr int NQ = N / SPT;
+    static constexpr int CH = kFwdThreads / NQ;          // channels a block
+    static constexpr int BATCH = NQ > kBatch ? NQ : kBatch;   // tokens whose u, dt and z a channel's lanes hold
+    static constexpr int OWN = BATCH / NQ;               // of them, a lane's: q, q + NQ, ...
+    static constexpr int BC = N / 4;                     // values of B and C a thread loads: 8 threads a token
 };
 
 // Sum of v[i] over the NQ lanes of a channel; lane q gets the sum of v[q].
@@ -79,37 +81,6 @@ __device__ __forceinline__ SsmBlock ssm_block(const SsmP &a, int CH) {
     return b;
 }
 
-// B and C of a tile: loads into registers, then FP32 into shared memory [kTile][N].
-template <typename T, int N>
-struct BcTile {
-    static constexpr int BE = SsmShape<N>::BE, PER = N / BE;
-    Raw<T, BE> b, c;
-    __device__ __forceinline__ void fetch(const SsmP &a, long long r0, int n, int g, bool with_c) {
-        const int t = threadIdx.x / PER, i = (threadIdx.x % PER) * BE;
-        const bool ok = t < n && t < kTile;
-        const T *pb = (const T *)a.Bm + (r0 + t) * a.ld_B + g * N + i;
-        b = ok && a.vecb ? load_raw<T, BE>(pb) : load_part<T, BE>(pb, ok ? BE : 0);
-        if (with_c) {
-            const T *pc = (const T *)a.Cm + (r0 + t) * a.ld_C + g * N + i;
-            c = ok && a.vecb ? load_raw<T, BE>(pc) : load_part<T, BE>(pc, ok ? BE : 0);
-        }
-    }
-    __device__ __forceinline__ void put(float *sB, float *sC) {
-        const int t = threadIdx.x / PER, i = (threadIdx.x % PER) * BE;
-        if (t < kTile) {
-            float v[BE];
-            widen<T, BE>(b, v);
-#pragma unroll
-            for (int k = 0; k < BE; ++k) sB[t * N + i + k] = v[k];
-            if (sC) {
-                widen<T, BE>(c, v);
-#pragma unroll
-                for (int k = 0; k < BE; ++k) sC[t * N + i + k] = v[k];
-            }
-        }
-    }
-};
-
 // 2^x of two values on the FMA pipe, which has room while the special-function unit (16 results a
 // clock and SM) is what the scans wait for.  x = n + f with f in [-1/2, 1/2]; 2^f = 1 + f p(f), p the
 // polynomial of degree 5 through (2^f - 1) / f at its Chebyshev points: the relative error is 2^-26.7
@@ -139,25 +110,25 @@ __device__ __forceinline__ float2 ex2_poly(float2 x) {
     return __fmul2_rn(p, s);
 }
 
-// Fills in sizes and layout; the kernels' own pointers are the launchers' to set.
-template <int N>
+// Fills in sizes and layout for blocks of CH channels, of which a thread takes EPT neighbouring ones
+// at a time, and BE values of B or C.  The kernels' own pointers are the launchers' to set.
+template <int CH, int EPT, int BE>
 SsmP ssm_params(const SsmArgs &a, int L) {
-    using S = SsmShape<N>;
     SsmP p = {};
     p.u = a.u; p.dt = a.dt; p.Bm = a.Bm; p.Cm = a.Cm; p.z = a.z; p.dout = a.dout;
     p.A = a.A; p.Dskip = a.Dskip; p.dt_bias = a.dt_bias; p.h0 = a.h0; p.dh_T = a.dh_T;
     p.out = a.out; p.du = a.du; p.ddt = a.ddt; p.dz = a.dz; p.h_T = a.h_T; p.dh0 = a.dh0;
     p.q.cu = a.cu; p.q.S = a.S; p.q.T = a.T;
     p.D = a.D; p.G = a.G; p.Dg = a.D / a.G;
-    p.cpg = (p.Dg + S::CH - 1) / S::CH;
+    p.cpg = (p.Dg + CH - 1) / CH;
     p.nblk = p.cpg * a.G;
     p.softplus = a.softplus;
-    long long ld = a.ld_u | a.ld_dt | (a.z ? a.ld_z : 0) | a.ld_out | p.Dg;
+    long long ld = a.ld_u | a.ld_dt | (a.z ? a.ld_z : 0) | a.ld_out;
     for (const void *r : {a.u, a.dt, a.z, (const void *)a.out, a.dout}) ld |= elements(r, a.bf16);
-    const int most = a.bf16 ? (S::EPT < 8 ? S::EPT : 8) : (S::EPT < 4 ? S::EPT : 4);
-    // a whole vector of EPT channels is in the group, or none of it, and is aligned
-    p.vec = ld % most == 0 && p.Dg % S::EPT == 0;
-    p.vecb = (a.ld_B | a.ld_C | elements(a.Bm, a.bf16) | elements(a.Cm, a.bf16)) % S::BE == 0;
+    // a whole vector of EPT channels is in the group, or none of it, and is aligned to 16 bytes or its size
+    const int per16 = a.bf16 ? 8 : 4;
+    p.vec = ld % (EPT < per16 ? EPT : per16) == 0 && p.Dg % EPT == 0;
+    p.vecb = (a.ld_B | a.ld_C | elements(a.Bm, a.bf16) | elements(a.Cm, a.bf16)) % (BE < per16 ? BE : per16) == 0;
     p.L = L;
     p.ld_u = a.ld_u; p.ld_dt = a.ld_dt; p.ld_z = a.ld_z; p.ld_B = a.ld_B; p.ld_C = a.ld_C; p.ld_out = a.ld_out;
     p.slots = span_slots(a.cu != nullptr, a.S, a.T, L);

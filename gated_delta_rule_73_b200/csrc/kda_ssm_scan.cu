@@ -25,20 +25,6 @@ namespace kda {
 namespace {
 
 // ---------------------------------------------------------------- a lane a channel
-constexpr int kFwdThreads = 128;
-constexpr int kBatch = 4;       // tokens whose u, dt and z a channel's lanes hold at a time
-
-// A channel's N states lie on NQ neighbouring lanes, SPT (at most 16) a lane.
-template <int N>
-struct FwdShape {
-    static constexpr int SPT = N < 16 ? N : 16;
-    static constexpr int NQ = N / SPT;
-    static constexpr int CH = kFwdThreads / NQ;          // channels a block
-    static constexpr int BATCH = NQ > kBatch ? NQ : kBatch;   // tokens whose u, dt and z a channel's lanes hold
-    static constexpr int OWN = BATCH / NQ;               // of them, a lane's: q, q + NQ, ...
-    static constexpr int BC = N / 4;                     // values of B and C a thread loads: 8 threads a token
-};
-
 template <typename T, int N, bool SWEEP>
 __global__ void __launch_bounds__(kFwdThreads, 4) ssm_fwd_kernel(const SsmP a) {
     using S = FwdShape<N>;
@@ -406,8 +392,10 @@ __global__ void __launch_bounds__(SeqShape<T, N>::THREADS, 2) ssm_seq_kernel(con
 
 // One thread per sequence and four states walks the spans: forward, hst[slot] goes from the
 // slot's own end to its start state; with gst, backward, gst[slot] goes from the gradient at the
-// span's start that its own outputs make to the gradient at its end that later spans make.
+// span's start that its own outputs make to the gradient at its end that later spans make.  Eight
+// spans' values are loaded ahead of the chain through them.
 __global__ void __launch_bounds__(128) ssm_seams_kernel(const SsmP a, int N) {
+    constexpr int U = 8;
     const long long per = (long long)a.D * N / 4;
     const long long id = (long long)blockIdx.x * 128 + threadIdx.x;
     if (id >= per * a.q.S) return;
@@ -416,39 +404,39 @@ __global__ void __launch_bounds__(128) ssm_seams_kernel(const SsmP a, int N) {
     const long long len = a.q.hi(s) - a.q.lo(s);
     const int count = len > 0 ? (int)((len + a.L - 1) / a.L) : 1;
     const long long slot0 = first_slot(a.q, s, a.L), all = (long long)a.D * N;
-    float A2[4];
+    const bool back = blockIdx.y != 0;
+    float A2[4], v[4] = {0.f, 0.f, 0.f, 0.f};
     load_f32<float, 4>(a.A + e, A2);
 #pragma unroll
     for (int i = 0; i < 4; ++i) A2[i] *= kLog2e;
-    if (blockIdx.y == 0) {
-        float h[4] = {0.f, 0.f, 0.f, 0.f};
-        if (a.h0) load_f32<float, 4>(a.h0 + s * all + e, h);
-        for (int k = 0; k < count - 1; ++k) {
-            float *p = a.hst + (slot0 + k) * all + e, end[4];
-            load_f32<float, 4>(p, end);
-            const float d = a.sdel[(slot0 + k) * a.D + c];
-            store_f32<float, 4>(p, h);
+    const float *from = back ? a.dh_T : a.h0;
+    if (from) load_f32<float, 4>(from + s * all + e, v);
+    float *seam = back ? a.gst : a.hst;
+    // the values that no span wrote, or that nothing needs: the last span's end, the first one's
+    // gradient where the start state has none
+    const int unread = back ? (a.dh0 ? -1 : 0) : count - 1;
+    for (int k0 = 0; k0 < count; k0 += U) {
+        float own[U][4], d[U];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = fmaf(ex2(A2[i] * d), h[i], end[i]);
-        }
-        store_f32<float, 4>(a.hst + (slot0 + count - 1) * all + e, h);
-    } else {
-        float g[4] = {0.f, 0.f, 0.f, 0.f};
-        if (a.dh_T) load_f32<float, 4>(a.dh_T + s * all + e, g);
-        for (int k = count - 1; k >= 0; --k) {
-            float *p = a.gst + (slot0 + k) * all + e, own[4] = {0.f, 0.f, 0.f, 0.f};
-            const bool on = len > 0 && (k > 0 || a.dh0);   // the others are not read, nor were they written
-            float d = 0.f;
-            if (on) {
-                load_f32<float, 4>(p, own);
-                d = a.sdel[(slot0 + k) * a.D + c];
+        for (int j = 0; j < U; ++j) {
+            const int k = back ? count - 1 - k0 - j : k0 + j;
+            d[j] = own[j][0] = own[j][1] = own[j][2] = own[j][3] = 0.f;
+            if (k >= 0 && k < count && k != unread && len > 0) {
+                load_f32<float, 4>(seam + (slot0 + k) * all + e, own[j]);
+                d[j] = a.sdel[(slot0 + k) * a.D + c];
             }
-            store_f32<float, 4>(p, g);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) g[i] = fmaf(ex2(A2[i] * d), g[i], own[i]);
         }
-        if (a.dh0) store_f32<float, 4>(a.dh0 + s * all + e, g);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int k = back ? count - 1 - k0 - j : k0 + j;
+            if (k >= 0 && k < count) {
+                store_f32<float, 4>(seam + (slot0 + k) * all + e, v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = fmaf(ex2(A2[i] * d[j]), v[i], own[j][i]);
+            }
+        }
     }
+    if (back && a.dh0) store_f32<float, 4>(a.dh0 + s * all + e, v);
 }
 
 template <typename T, int N>
@@ -526,14 +514,7 @@ FwdPlan plan(const SsmArgs &a) {
 template <typename T, int N>
 cudaError_t run_seq(const SsmArgs &a, cudaStream_t st) {
     using S = SeqShape<T, N>;
-    SsmP p = ssm_params<N>(a, a.T > 0 ? (int)a.T : 1);
-    p.cpg = (p.Dg + S::CH - 1) / S::CH;
-    p.nblk = p.cpg * a.G;
-    long long ld = a.ld_u | a.ld_dt | (a.z ? a.ld_z : 0) | a.ld_out | p.Dg;
-    for (const void *r : {a.u, a.dt, a.z, (const void *)a.out}) ld |= elements(r, a.bf16);
-    p.vec = ld % S::EV == 0;
-    constexpr int most = S::VB * sizeof(T) < 16 ? S::VB : 16 / sizeof(T);
-    p.vecb = (a.ld_B | a.ld_C | elements(a.Bm, a.bf16) | elements(a.Cm, a.bf16)) % most == 0;
+    const SsmP p = ssm_params<S::CH, S::EV, S::VB>(a, a.T > 0 ? (int)a.T : 1);
     const long long blocks = p.slots * p.nblk;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     constexpr int smem = sizeof(typename S::Stage) * S::STAGES;
@@ -549,11 +530,7 @@ cudaError_t run_fwd(const SsmArgs &a, cudaStream_t st) {
     const FwdPlan f = plan(a);
     if (f.lanes) return run_seq<T, N>(a, st);
     using F = FwdShape<N>;
-    SsmP p = ssm_params<N>(a, f.L);
-    p.cpg = (p.Dg + F::CH - 1) / F::CH;
-    p.nblk = p.cpg * a.G;
-    constexpr int most = F::BC * sizeof(T) < 16 ? F::BC : 16 / sizeof(T);
-    p.vecb = (a.ld_B | a.ld_C | elements(a.Bm, a.bf16) | elements(a.Cm, a.bf16)) % most == 0;
+    SsmP p = ssm_params<F::CH, 1, F::BC>(a, f.L);
     const long long blocks = p.slots * p.nblk;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (p.L < a.T) {
@@ -571,7 +548,7 @@ cudaError_t run_fwd(const SsmArgs &a, cudaStream_t st) {
 }
 template <typename T, int N>
 cudaError_t run_step(const SsmArgs &a, cudaStream_t st) {
-    const SsmP p = ssm_params<N>(a, 1);
+    const SsmP p = ssm_params<1, 1, 1>(a, 1);
     const long long blocks = ((long long)a.S * a.D * (N / 4) + 127) / 128;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     a.marks->mark(st);
