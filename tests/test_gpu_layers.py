@@ -318,6 +318,14 @@ NORM = [
     ((2,), 16384, True, True, True, 0),
     ((2,), 16383, True, True, True, 0),
     ((700,), 72, True, True, True, 0),
+    ((150,), 1000, True, True, True, 0),
+    ((150,), 1500, True, False, True, 4),
+    ((149,), 2056, True, True, False, 0),
+    ((149,), 3001, True, True, True, 0),
+    ((149,), 8184, True, True, True, 0),
+    ((149,), 8001, False, False, True, 0),
+    ((1300,), 1032, True, True, True, 0),
+    ((4000,), 40, True, True, True, 0),
     ((4,), 256, False, False, True, 0),
     ((0,), 256, True, True, True, 0),
 ] if torch.cuda.is_available() else []
