@@ -56,6 +56,11 @@ __device__ __forceinline__ float reduce_states(float (&v)[NQ], int q) {
     return v[0];
 }
 
+// Where chunk c of a row of lanes' parts lies: eight threads that read chunks 2, 4 or 8 apart find
+// them in different banks.  Chunks c to c + 7 of a thread that starts at a multiple c of 8 lie at
+// spread(c) ^ 0 .. spread(c) ^ 7.
+__device__ __forceinline__ int spread(int c) { return c ^ ((c >> 3) & 7); }
+
 // The raw values of one tensor that a thread loads for its token and EPT channels.
 template <typename T, int EPT>
 __device__ __forceinline__ Raw<T, EPT> load_tile(const void *p, long long row, long long ld, int c, int left,

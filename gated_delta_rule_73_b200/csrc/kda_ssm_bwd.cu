@@ -571,41 +571,52 @@ __global__ void __launch_bounds__(kBwdThreads, 3) ssm_bwd_kernel(const SsmP a) {
     }
 }
 
-// The last sums, in a fixed order: dB and dC of a row over its group's channel blocks, a thread a
-// value; dA, dDskip and ddt_bias over the spans, 32 columns a block and 8 spans at a time.
+// The last sums, in a fixed order: dB and dC over a group's channel blocks, 128 values a block of
+// threads; dA, dDskip and ddt_bias over the spans, 32 columns.  Eight warps share the terms.
 template <typename T>
 __global__ void __launch_bounds__(256) ssm_bwd_sum_kernel(const SsmP a, T *dB, T *dC, float *dA, float *dDskip,
                                                           float *ddt_bias, int N, unsigned bc_blocks) {
+    __shared__ float4 sums[8][32];
+    const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
     if (blockIdx.x < bc_blocks) {
-        const long long per = (long long)a.G * 2 * N, rows = a.q.rows();
-        const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-        const long long row = id / per;
-        if (row >= rows) return;
+        const long long rows = a.q.rows(), all = rows * 2 * N;   // values of a channel block
+        const long long i = ((long long)blockIdx.x * 32 + lane) * 4;
+        const int g = (int)(i / all);
+        const long long in = i % all, row = in / (2 * N);        // a quad lies in one row, in B or in C
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (g < a.G) {
+            const float *p = a.part_BC + (long long)g * a.cpg * all + in;
+#pragma unroll 4
+            for (int m = y; m < a.cpg; m += 8) {
+                const float4 w = *reinterpret_cast<const float4 *>(p + m * all);
+                v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+            }
+        }
+        sums[y][lane] = v;
+        __syncthreads();
+        if (y > 0 || g >= a.G) return;
         if (a.q.cu && (row < a.q.lo(0) || row >= a.q.lo(a.q.S))) return;   // of no sequence: not written
-        const int k = (int)(id % per), g = k / (2 * N), i = k % (2 * N);
-        const float *p = a.part_BC + ((long long)g * a.cpg * rows + row) * (2 * N) + i;
-        float v = 0.f;
-#pragma unroll 16
-        for (int m = 0; m < a.cpg; ++m) v += p[(long long)m * rows * (2 * N)];
-        const long long o = (row * a.G + g) * N;
-        if (i < N) dB[o + i] = from_f32<T>(v);
-        else dC[o + i - N] = from_f32<T>(v);
+#pragma unroll
+        for (int m = 1; m < 8; ++m) {
+            const float4 w = sums[m][lane];
+            v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+        }
+        const int k = (int)(in % (2 * N));
+        const float f[4] = {v.x, v.y, v.z, v.w};
+        store_f32<T, 4>((k < N ? dB + k : dC + k - N) + (row * a.G + g) * N, f);
         return;
     }
-    __shared__ float sums[8][32];
     const long long n = (long long)a.D * (N + 2), all = (long long)a.D * N;
-    const long long i = (long long)(blockIdx.x - bc_blocks) * 32 + (threadIdx.x & 31);
-    const int y = threadIdx.x >> 5;
+    const long long i = (long long)(blockIdx.x - bc_blocks) * 32 + lane;
     float v = 0.f;
     if (i < n)
 #pragma unroll 8
         for (long long k = y; k < a.slots; k += 8) v += a.part[k * a.part_ld + i];
-    sums[y][threadIdx.x & 31] = v;
+    sums[y][lane].x = v;
     __syncthreads();
     if (y == 0 && i < n) {
-        v = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v += sums[k][threadIdx.x];
+        for (int k = 1; k < 8; ++k) v += sums[k][lane].x;
         if (i < all) dA[i] = v;
         else if (i < all + a.D) {
             if (dDskip) dDskip[i - all] = v;
@@ -654,7 +665,7 @@ cudaError_t run(const SsmArgs &a, cudaStream_t st) {
     p.part_ld = part_ld(a);
     const long long blocks = p.slots * p.nblk;
     const long long sweep_blocks = p.slots * a.G * ((p.Dg + F::CH - 1) / F::CH);
-    const long long bc_blocks = (a.rows * a.G * 2 * N + 255) / 256, sum_blocks = ((long long)a.D * (N + 2) + 31) / 32;
+    const long long bc_blocks = (a.rows * a.G * 2 * N + 127) / 128, sum_blocks = ((long long)a.D * (N + 2) + 31) / 32;
     if (blocks > 0x7fffffffLL || sweep_blocks > 0x7fffffffLL || bc_blocks + sum_blocks > 0x7fffffffLL)
         return cudaErrorInvalidValue;
     constexpr int smem = sizeof(typename S::Smem);

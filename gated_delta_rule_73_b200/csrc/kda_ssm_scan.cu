@@ -193,10 +193,6 @@ __device__ __forceinline__ void wait_at(int id) { asm volatile("bar.sync %0, %1;
 template <int THREADS>
 __device__ __forceinline__ void arrive_at(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(THREADS) : "memory"); }
 
-// Where the 16-byte chunk c of a row of parts lies: eight threads that read chunks 2 or 4 apart
-// find them in different banks.
-__device__ __forceinline__ int spread(int c) { return (c & ~7) | ((c + (c >> 3)) & 7); }
-
 template <typename T, int N>
 struct SeqShape {
     static constexpr int SPT = 4;                      // states a lane
