@@ -15,6 +15,7 @@ using namespace kda;
 namespace {
 
 constexpr long long kMaxElems = 1LL << 40;   // refuse sizes whose byte offsets could overflow
+constexpr long long kMaxRows = 0x7fffff00LL;  // a few rows more still fit an int
 constexpr long long kMaxStride = 1LL << 27;  // a few rows' offsets fit 32 bits of bytes
 
 kda_opts resolve(const kda_opts *o) {
@@ -65,7 +66,7 @@ int stride(long long &ld, long long length) {
 int check_rows(int B, int T, bool packed, long long widest, long long *rows) {
     if (B < 0 || T < 0) return KDA_ERR_ARG;
     *rows = packed ? T : (long long)B * T;
-    if (*rows > 0x7fffffffLL) return KDA_ERR_SHAPE;
+    if (*rows > kMaxRows) return KDA_ERR_SHAPE;
     if (*rows > 0 && widest > kMaxElems / *rows) return KDA_ERR_SHAPE;
     return KDA_OK;
 }

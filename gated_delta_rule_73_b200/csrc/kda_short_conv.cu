@@ -211,10 +211,11 @@ __device__ __forceinline__ void dpre_of(const float2 (&p)[P], float2 (&g)[P], bo
 
 // A walk owns the rows r0 .. r1-1: it writes their dx, for which it needs dpre up to K-1 rows
 // on, and sums dpre and dpre x over its own rows into its partial sums [walk][K + 1][D].  One pair
-// of channels a thread: its 2 K + 2 sums, taps and rows take 60 registers, and the warps that fit
-// hide most of HBM's latency: 72 us for 16384 x 2048 in bf16, 110 with two pairs a thread.
+// of channels a thread: its 2 K + 2 sums, taps and rows take 60 registers, and the 20 warps an
+// SM that fit hide most of HBM's latency: 64 us for 16384 x 2048 in bf16, 72 with 16 warps, 110 with
+// two pairs a thread.
 template <typename T, int K, bool V>
-__global__ void __launch_bounds__(kThreads) short_conv_bwd_kernel(const ConvP a) {
+__global__ void __launch_bounds__(kThreads, 5) short_conv_bwd_kernel(const ConvP a) {
     constexpr int P = 1;
     const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
     const long long walk = id / a.groups;
@@ -264,11 +265,11 @@ __global__ void __launch_bounds__(kThreads) short_conv_bwd_kernel(const ConvP a)
     for (int j = 0; j <= K; ++j)
 #pragma unroll
         for (int i = 0; i < P; ++i) dw[j][i] = make_float2(0.f, 0.f);
-    long long r = walk * a.L;
-    const long long rows = a.q.rows(), r1 = r + a.L < rows ? r + a.L : rows;
+    int r = (int)(walk * a.L);
+    const int r1 = (int)(a.q.rows() - r < a.L ? a.q.rows() : r + a.L);
     int s = a.q.at(r);
     while (r < r1) {
-        const long long lo = a.q.lo(s), hi = a.q.hi(s);
+        const int lo = (int)a.q.lo(s), hi = (int)a.q.hi(s);
         if (r >= hi) {
             if (++s >= a.q.S) break;
             continue;
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) short_conv_bwd_kernel(const ConvP a)
             r = lo;
             continue;
         }
-        const long long e = hi < r1 ? hi : r1;
+        const int e = hi < r1 ? hi : r1;
         float2 win[K - 1][P], ring[K - 1][P];   // inputs before row p; dpre of the rows before it
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) {
@@ -285,8 +286,8 @@ __global__ void __launch_bounds__(kThreads) short_conv_bwd_kernel(const ConvP a)
 #pragma unroll
             for (int i = 0; i < P; ++i) ring[j][i] = make_float2(0.f, 0.f);
         }
-        const T *px = x + r * a.ld_x, *pg = dy + r * a.ld_y;
-        T *po = (T *)a.dx + c + (r - (K - 1)) * a.ld_dx;
+        const T *px = x + (long long)r * a.ld_x, *pg = dy + (long long)r * a.ld_y;
+        T *po = (T *)a.dx + c + (long long)(r - (K - 1)) * a.ld_dx;
         // A row's dpre d, and dx of the row K-1 before it, whose last term it is.
         auto gather = [&](const float2 (&d)[P], float2 (&o)[P]) {
 #pragma unroll
@@ -312,8 +313,8 @@ __global__ void __launch_bounds__(kThreads) short_conv_bwd_kernel(const ConvP a)
             }
             push(win, v);
         };
-        auto put = [&](long long t, T *o, float2 (&v)[P]) {   // dx of row t, with what the last state adds
-            const long long back = t - hi + (K - 1);
+        auto put = [&](int t, T *o, float2 (&v)[P]) {   // dx of row t, with what the last state adds
+            const int back = t - hi + (K - 1);
             if (a.dstate_T && back >= 0) {
                 Row<float, P, V> g;
                 float2 f[P];
@@ -324,9 +325,9 @@ __global__ void __launch_bounds__(kThreads) short_conv_bwd_kernel(const ConvP a)
             }
             store_row<T, P, V>(o, v, have);
         };
-        long long p = r;
+        int p = r;
         // Whole batches inside the walk.  (With the next batch loaded while one is computed the registers
-        // leave fewer warps: 77 to 87 us for 16384 x 2048 in bf16, against 72.)
+        // leave fewer warps: 77 to 87 us for 16384 x 2048 in bf16.)
         constexpr int U = 8;
         for (; p + U <= e; p += U) {
             Row<T, P, V> rx[U], rg[U];
@@ -460,8 +461,8 @@ int fwd_rows(long long rows, int groups) {
 // Rows a backward walk takes; at least 16, so that the partial sums of (K + 1) FP32 values a
 // channel and walk stay small against the rows' bytes.
 int bwd_rows(long long rows, int D) {
-    int L = 128;
-    while (L > 16 && ceil_div(rows, L) * (D / 2) < (1 << 17)) L /= 2;
+    int L = 64;
+    while (L > 16 && ceil_div(rows, L) * (D / 2) < (1 << 18)) L /= 2;
     return L;
 }
 

@@ -20,11 +20,11 @@
  * none.  Bounds outside 0 .. T are clamped on the device.  Rows of no sequence are neither
  * read nor written, unless zero_rest is set: then the call's row outputs are zero there.
  *
- * Row strides (ld_*) count elements; 0 means the row's own length (contiguous); at
- * most 2^27.  A tensor
- * with a row stride may so be a column range of a wider one, and unlike the others it may
- * start at any element; 16-byte aligned rows are read in wider accesses. Inputs and outputs must not overlap unless a
- * comment says so; where pointers show it, the call is refused (KDA_ERR_ARG).
+ * At most 2^31 - 256 rows.  Row strides (ld_*) count elements, at most 2^27; 0 means the
+ * row's own length (contiguous).  A tensor with a row stride may so be a column range of a
+ * wider one, and unlike the others it may start at any element; rows at 16 bytes are read in
+ * wider accesses.  Inputs and outputs must not overlap unless a comment says so; where
+ * pointers show it, the call is refused (KDA_ERR_ARG).
  *
  * Gradients of activations have the activation type, gradients of parameters and states
  * are FP32; all are written, not accumulated, and every sum has a fixed order.
