@@ -123,7 +123,7 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) {
 }
 
 template <typename T, int P, int K, bool V>
-__global__ void __launch_bounds__(kThreads) short_conv_fwd_kernel(const ConvP a) {
+__global__ void __launch_bounds__(kThreads, 5) short_conv_fwd_kernel(const ConvP a) {
     const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
     const long long walk = id / a.groups;
     const int c = (int)(id % a.groups) * 2 * P, have = a.D - c < 2 * P ? a.D - c : 2 * P;
@@ -141,11 +141,11 @@ __global__ void __launch_bounds__(kThreads) short_conv_fwd_kernel(const ConvP a)
     }
     Taps<T, P, K, V> taps;
     taps.load(a, c, have);
-    long long r = walk * a.L;
-    const long long rows = a.q.rows(), r1 = r + a.L < rows ? r + a.L : rows;
+    int r = (int)(walk * a.L);
+    const int r1 = (int)(a.q.rows() - r < a.L ? a.q.rows() : r + a.L);
     int s = a.q.at(r);
     while (r < r1) {
-        const long long lo = a.q.lo(s), hi = a.q.hi(s);
+        const int lo = (int)a.q.lo(s), hi = (int)a.q.hi(s);
         if (r >= hi) {   // on to the next sequence, past empty ones
             if (++s >= a.q.S) break;
             continue;
@@ -157,9 +157,9 @@ __global__ void __launch_bounds__(kThreads) short_conv_fwd_kernel(const ConvP a)
         float2 win[K - 1][P];
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) load_row<T, P, K, V>(a, s, lo, r - (K - 1) + j, c, have, win[j]);
-        const long long e = hi < r1 ? hi : r1;
-        const T *px = (const T *)a.x + r * a.ld_x + c;
-        T *py = (T *)a.y + r * a.ld_y + c;
+        const int e = hi < r1 ? hi : r1;
+        const T *px = (const T *)a.x + (long long)r * a.ld_x + c;
+        T *py = (T *)a.y + (long long)r * a.ld_y + c;
         auto row = [&](const Row<T, P, V> &raw, T *o) {
             float2 v[P], p[P];
             raw.get(v);
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) short_conv_fwd_kernel(const ConvP a)
             }
             store_row<T, P, V>(o, p, have);
         };
-        constexpr int U = 4;   // rows a batch; the next one is loaded while one is computed
+        constexpr int U = V ? 8 : 4;  // rows a batch; the next one is loaded while one is computed
         Row<T, P, V> cur[U], next[U];
         if (r + U <= e)
 #pragma unroll
