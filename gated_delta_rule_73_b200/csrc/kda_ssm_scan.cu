@@ -310,22 +310,24 @@ __global__ void __launch_bounds__(SeqShape<T, N>::THREADS, 2) ssm_seq_kernel(con
     const T *pbc = is_b ? (const T *)a.Bm + (b.sp.r0 + bt) * a.ld_B + b.g * N + bk
                         : (const T *)a.Cm + (b.sp.r0 + bt) * a.ld_C + b.g * N + bk - N;
     const long long ldbc = is_b ? a.ld_B : a.ld_C;
-    Raw<T, EV> nu[PASS], nd[PASS], nz[PASS];
-    Raw<T, VB> nbc;
-    auto fetch = [&](int t0) {
+    constexpr int DEPTH = 2;   // a tile's loads are two tiles on the way: a tile takes a microsecond, HBM's latency is more
+    struct Next {
+        Raw<T, EV> u[PASS], d[PASS], z[PASS];
+        Raw<T, VB> bc;
+    } next[DEPTH];
+    auto fetch = [&](Next &x, int t0) {
 #pragma unroll
         for (int p = 0; p < PASS; ++p) {
             const int t = t0 + p * TSTEP + lt;
             const bool ok = t < n && p * TSTEP + lt < TT;
-            nu[p] = load_tile<T, EV>(a.u, b.sp.r0 + t, a.ld_u, c, left, ok, a.vec);
-            nd[p] = load_tile<T, EV>(a.dt, b.sp.r0 + t, a.ld_dt, c, left, ok, a.vec);
-            if (gate) nz[p] = load_tile<T, EV>(a.z, b.sp.r0 + t, a.ld_z, c, left, ok, a.vec);
+            x.u[p] = load_tile<T, EV>(a.u, b.sp.r0 + t, a.ld_u, c, left, ok, a.vec);
+            x.d[p] = load_tile<T, EV>(a.dt, b.sp.r0 + t, a.ld_dt, c, left, ok, a.vec);
+            if (gate) x.z[p] = load_tile<T, EV>(a.z, b.sp.r0 + t, a.ld_z, c, left, ok, a.vec);
         }
         const bool ok = t0 + bt < n;
-        nbc = ok && a.vecb ? load_raw<T, VB>(pbc + t0 * ldbc) : load_part<T, VB>(pbc + t0 * ldbc, ok ? VB : 0);
+        x.bc = ok && a.vecb ? load_raw<T, VB>(pbc + t0 * ldbc) : load_part<T, VB>(pbc + t0 * ldbc, ok ? VB : 0);
     };
-    fetch(0);
-    for (int i = 0; i < tiles + 2; ++i) {
+    auto tile = [&](int i, Next &cur) {
         if (i < tiles) {
             typename S::Stage &s = stage[i % ST];
             const int t0 = i * TT;
@@ -334,8 +336,8 @@ __global__ void __launch_bounds__(SeqShape<T, N>::THREADS, 2) ssm_seq_kernel(con
                 const int t = p * TSTEP + lt;
                 if (t >= TT) break;
                 float u[EV], d[EV], x[2 * EV];
-                widen<T, EV>(nu[p], u);
-                widen<T, EV>(nd[p], d);
+                widen<T, EV>(cur.u[p], u);
+                widen<T, EV>(cur.d[p], d);
 #pragma unroll
                 for (int k = 0; k < EV; ++k) {
                     d[k] += bias[k];
@@ -345,13 +347,13 @@ __global__ void __launch_bounds__(SeqShape<T, N>::THREADS, 2) ssm_seq_kernel(con
                     x[2 * k + 1] = d[k] * u[k];
                 }
                 store_f32<float, 2 * EV>(&s.x[t][lc].x, x);
-                store_raw<T, EV>(&s.u[t][lc], nu[p]);
-                if (gate) store_raw<T, EV>(&s.z[t][lc], nz[p]);
+                store_raw<T, EV>(&s.u[t][lc], cur.u[p]);
+                if (gate) store_raw<T, EV>(&s.z[t][lc], cur.z[p]);
             }
             float v[VB];
-            widen<T, VB>(nbc, v);
+            widen<T, VB>(cur.bc, v);
             store_f32<float, VB>(&s.bc[bt][bk], v);
-            if (i + 1 < tiles) fetch(t0 + TT);
+            if (i + DEPTH < tiles) fetch(cur, t0 + DEPTH * TT);
             arrive_at<ALL>(FULL + i % ST);
         }
         if (i >= 2) {
@@ -383,7 +385,13 @@ __global__ void __launch_bounds__(SeqShape<T, N>::THREADS, 2) ssm_seq_kernel(con
                 else store_part<T, EV>(o, y, left);
             }
         }
-    }
+    };
+#pragma unroll
+    for (int j = 0; j < DEPTH; ++j) fetch(next[j], j * TT);
+    for (int i = 0; i < tiles + 2; i += DEPTH)
+#pragma unroll
+        for (int j = 0; j < DEPTH; ++j)
+            if (i + j < tiles + 2) tile(i + j, next[j]);
 }
 
 // One thread per sequence and four states walks the spans: forward, hst[slot] goes from the
