@@ -45,16 +45,38 @@ bool rows_aligned(bool bf16, std::initializer_list<const void *> ps) {
         if ((uintptr_t)p & (bf16 ? 1u : 3u)) return false;
     return true;
 }
-// outputs against the inputs and against each other; NULL is nobody's
-bool distinct(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins) {
-    for (const void *const *o = outs.begin(); o != outs.end(); ++o) {
-        if (!*o) continue;
-        for (const void *i : ins)
-            if (*o == i) return false;
-        for (const void *const *p = outs.begin(); p != o; ++p)
-            if (*o == *p) return false;
+// A tensor's memory: rows of `width` bytes, `ld` apart.  A NULL pointer or no bytes: none.
+struct Mem {
+    const char *p;
+    long long rows, ld, width;
+};
+Mem flat(const void *p, long long bytes) { return {(const char *)p, 1, bytes, bytes}; }
+Mem rows_of(const void *p, long long rows, long long ld, long long width, bool bf16) {
+    const long long e = bf16 ? 2 : 4;
+    return {(const char *)p, rows, ld * e, width * e};
+}
+bool overlap(const Mem &a, const Mem &b) {
+    if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+    const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+    if (pb >= pa + (a.rows - 1) * a.ld + a.width || pa >= pb + (b.rows - 1) * b.ld + b.width) return false;
+    if (a.ld != b.ld) return true;
+    // column ranges of rows equally far apart
+    const long long d = (long long)((pb >= pa ? pb - pa : (uintptr_t)a.ld - (pa - pb) % a.ld) % a.ld);
+    return !(d >= a.width && d + b.width <= a.ld);
+}
+// outputs against the inputs and against each other
+bool distinct(std::initializer_list<Mem> outs, std::initializer_list<Mem> ins) {
+    for (const Mem *o = outs.begin(); o != outs.end(); ++o) {
+        for (const Mem &i : ins)
+            if (overlap(*o, i)) return false;
+        for (const Mem *p = outs.begin(); p != o; ++p)
+            if (overlap(*o, *p)) return false;
     }
     return true;
+}
+// all of `p`, or nothing of it, is `q`: in place
+bool same_or_apart(const Mem &p, const Mem &q) {
+    return (p.p == q.p && p.rows == q.rows && p.ld == q.ld && p.width == q.width) || !overlap(p, q);
 }
 
 // A row stride: 0 stands for the row's own length.
@@ -83,6 +105,7 @@ int conv_dims(const kda_conv_dims *d, const kda_opts &o, bool step, ConvArgs &a)
     if ((d->silu | 1) != 1 || (d->zero_rest | 1) != 1) return KDA_ERR_ARG;
     if (d->K < 2 || d->K > 4) return KDA_ERR_UNSUPPORTED;
     a.cu = step ? nullptr : d->cu_seqlens;
+    if ((uintptr_t)a.cu & 3u) return KDA_ERR_ALIGN;
     a.S = d->B; a.D = d->D; a.K = d->K; a.silu = d->silu;
     a.T = step ? 1 : d->T;
     a.ld_x = d->ld_x; a.ld_y = d->ld_y; a.ld_dx = d->ld_dx;
@@ -106,6 +129,7 @@ int ssm_dims(const kda_ssm_dims *d, const kda_opts &o, bool step, SsmArgs &a) {
     if (d->N != 8 && d->N != 16 && d->N != 32 && d->N != 64) return KDA_ERR_UNSUPPORTED;
     if (d->D % d->G) return KDA_ERR_SHAPE;
     a.cu = step ? nullptr : d->cu_seqlens;
+    if ((uintptr_t)a.cu & 3u) return KDA_ERR_ALIGN;
     a.S = d->B; a.D = d->D; a.N = d->N; a.G = d->G; a.softplus = d->dt_softplus;
     a.T = step ? 1 : d->T;
     a.ld_u = d->ld_u; a.ld_dt = d->ld_dt; a.ld_z = d->ld_z; a.ld_B = d->ld_B; a.ld_C = d->ld_C; a.ld_out = d->ld_out;
@@ -170,13 +194,16 @@ int kda_short_conv_fwd(const void *x, const void *w, const void *bias, const voi
     if (!w || (a.rows > 0 && (!x || !y))) return KDA_ERR_ARG;
     if (!all_aligned({w, bias, state0, state_T}) || !rows_aligned(a.bf16, {x, y}))
         return KDA_ERR_ALIGN;
-    if (!distinct({y, state_T}, {x, w, bias, state0, a.cu})) return KDA_ERR_ARG;
+    const long long es = a.bf16 ? 2 : 4, ns = (long long)a.S * (a.K - 1) * a.D, D = a.D;
+    if (!distinct({rows_of(y, a.rows, a.ld_y, D, a.bf16), flat(state_T, ns * es)},
+                  {rows_of(x, a.rows, a.ld_x, D, a.bf16), flat(w, D * a.K * es), flat(bias, D * es), flat(state0, ns * es),
+                   flat(a.cu, a.cu ? 4LL * (a.S + 1) : 0)}))
+        return KDA_ERR_ARG;
     a.x = x; a.w = w; a.bias = bias; a.state0 = state0; a.y = y; a.state_T = state_T;
     LaunchMarks m = marks_of(o);
     a.marks = &m;
     cudaError_t e = a.S > 0 ? launch_short_conv_fwd(a, stream) : cudaSuccess;
     if (e == cudaSuccess && a.cu && dims->zero_rest && a.rows > 0) {
-        const long long es = a.bf16 ? 2 : 4;
         const ZeroRest z = {{y}, {a.D * es}, {a.ld_y * es}, 1};
         m.mark(stream);
         e = launch_zero_rest(z, a.cu, a.S, a.T, stream);
@@ -197,8 +224,13 @@ int kda_short_conv_bwd(const void *x, const void *w, const void *bias, const voi
     if (!all_aligned({w, bias, state0, dstate_T, dw, dbias, dstate0, o.workspace}) ||
         !rows_aligned(a.bf16, {x, dy, dx}))
         return KDA_ERR_ALIGN;
-    if (!distinct({dx, dw, dbias, dstate0, o.workspace}, {x, w, bias, state0, dy, dstate_T, a.cu})) return KDA_ERR_ARG;
     const size_t need = short_conv_bwd_workspace_bytes(a.rows, a.D, a.K);
+    const long long es = a.bf16 ? 2 : 4, ns = (long long)a.S * (a.K - 1) * a.D, D = a.D;
+    if (!distinct({rows_of(dx, a.rows, a.ld_dx, D, a.bf16), flat(dw, D * a.K * 4), flat(dbias, D * 4), flat(dstate0, ns * 4),
+                   flat(o.workspace, (long long)need)},
+                  {rows_of(x, a.rows, a.ld_x, D, a.bf16), flat(w, D * a.K * es), flat(bias, D * es), flat(state0, ns * es),
+                   rows_of(dy, a.rows, a.ld_y, D, a.bf16), flat(dstate_T, ns * 4), flat(a.cu, a.cu ? 4LL * (a.S + 1) : 0)}))
+        return KDA_ERR_ARG;
     if (need > 0 && (!o.workspace || o.workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     a.x = x; a.w = w; a.bias = bias; a.state0 = state0; a.dy = dy; a.dstate_T = dstate_T;
     a.dx = dx; a.dw = dw; a.dbias = dbias; a.dstate0 = dstate0;
@@ -213,7 +245,6 @@ int kda_short_conv_bwd(const void *x, const void *w, const void *bias, const voi
         if (e == cudaSuccess) e = zero_f32(dbias, a.D, stream);
     }
     if (e == cudaSuccess && a.cu && dims->zero_rest && a.rows > 0) {
-        const long long es = a.bf16 ? 2 : 4;
         const ZeroRest z = {{dx}, {a.D * es}, {a.ld_dx * es}, 1};
         m.mark(stream);
         e = launch_zero_rest(z, a.cu, a.S, a.T, stream);
@@ -232,7 +263,11 @@ int kda_short_conv_step(const void *x, const void *w, const void *bias, const vo
     if (!x || !w || !state || !state_out || !y) return KDA_ERR_ARG;
     if (!all_aligned({w, bias, state, state_out}) || !rows_aligned(a.bf16, {x, y}))
         return KDA_ERR_ALIGN;
-    if (!distinct({y, state_out}, {x, w, bias}) || y == state) return KDA_ERR_ARG;
+    const long long es = a.bf16 ? 2 : 4, ns = (long long)a.S * (a.K - 1) * a.D, D = a.D;
+    const Mem my = rows_of(y, a.rows, a.ld_y, D, a.bf16), so = flat(state_out, ns * es), si = flat(state, ns * es);
+    if (!distinct({my, so}, {rows_of(x, a.rows, a.ld_x, D, a.bf16), flat(w, D * a.K * es), flat(bias, D * es)}) ||
+        overlap(my, si) || !same_or_apart(so, si))
+        return KDA_ERR_ARG;
     a.x = x; a.w = w; a.bias = bias; a.state0 = state; a.state_T = state_out; a.y = y;
     LaunchMarks m = marks_of(o);
     a.marks = &m;
@@ -266,8 +301,13 @@ int kda_ssm_scan_fwd(const void *u, const void *dt, const float *A, const void *
     if (!all_aligned({A, Dskip, dt_bias, h0, h_T, o.workspace}) ||
         !rows_aligned(a.bf16, {u, dt, Bm, Cm, z, out}))
         return KDA_ERR_ALIGN;
-    if (!distinct({out, h_T, o.workspace}, {u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, a.cu})) return KDA_ERR_ARG;
     const size_t need = a.S > 0 ? ssm_scan_fwd_workspace_bytes(a) : 0;
+    const long long es = a.bf16 ? 2 : 4, D = a.D, bc = (long long)a.G * a.N, ns = (long long)a.S * D * a.N * 4;
+    if (!distinct({rows_of(out, a.rows, a.ld_out, D, a.bf16), flat(h_T, ns), flat(o.workspace, (long long)need)},
+                  {rows_of(u, a.rows, a.ld_u, D, a.bf16), rows_of(dt, a.rows, a.ld_dt, D, a.bf16), rows_of(z, a.rows, a.ld_z, D, a.bf16),
+                   rows_of(Bm, a.rows, a.ld_B, bc, a.bf16), rows_of(Cm, a.rows, a.ld_C, bc, a.bf16), flat(A, D * a.N * 4),
+                   flat(Dskip, D * 4), flat(dt_bias, D * 4), flat(h0, ns), flat(a.cu, a.cu ? 4LL * (a.S + 1) : 0)}))
+        return KDA_ERR_ARG;
     if (need > 0 && (!o.workspace || o.workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     a.u = u; a.dt = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.Dskip = Dskip; a.z = z; a.dt_bias = dt_bias;
     a.h0 = h0; a.out = out; a.h_T = h_T; a.workspace = o.workspace;
@@ -275,7 +315,6 @@ int kda_ssm_scan_fwd(const void *u, const void *dt, const float *A, const void *
     a.marks = &m;
     cudaError_t e = a.S > 0 ? launch_ssm_scan_fwd(a, stream) : cudaSuccess;
     if (e == cudaSuccess && a.cu && dims->zero_rest && a.rows > 0) {
-        const long long es = a.bf16 ? 2 : 4;
         const ZeroRest zr = {{out}, {a.D * es}, {a.ld_out * es}, 1};
         m.mark(stream);
         e = launch_zero_rest(zr, a.cu, a.S, a.T, stream);
@@ -299,10 +338,16 @@ int kda_ssm_scan_bwd(const void *u, const void *dt, const float *A, const void *
     if (!all_aligned({A, Dskip, dt_bias, h0, dh_T, du, ddt, dA, dB, dC, dDskip, dz, ddt_bias, dh0, o.workspace}) ||
         !rows_aligned(a.bf16, {u, dt, Bm, Cm, z, dout}))
         return KDA_ERR_ALIGN;
-    if (!distinct({du, ddt, dA, dB, dC, dDskip, dz, ddt_bias, dh0, o.workspace},
-                  {u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, dout, dh_T, a.cu}))
-        return KDA_ERR_ARG;
     const size_t need = ssm_scan_bwd_workspace_bytes(a);
+    const long long es = a.bf16 ? 2 : 4, D = a.D, bc = (long long)a.G * a.N, ns = (long long)a.S * D * a.N * 4;
+    const long long nd = a.rows * D * es, nbc = a.rows * bc * es;
+    if (!distinct({flat(du, nd), flat(ddt, nd), flat(dz, nd), flat(dB, nbc), flat(dC, nbc), flat(dA, D * a.N * 4),
+                   flat(dDskip, D * 4), flat(ddt_bias, D * 4), flat(dh0, ns), flat(o.workspace, (long long)need)},
+                  {rows_of(u, a.rows, a.ld_u, D, a.bf16), rows_of(dt, a.rows, a.ld_dt, D, a.bf16), rows_of(z, a.rows, a.ld_z, D, a.bf16),
+                   rows_of(Bm, a.rows, a.ld_B, bc, a.bf16), rows_of(Cm, a.rows, a.ld_C, bc, a.bf16), flat(A, D * a.N * 4),
+                   flat(Dskip, D * 4), flat(dt_bias, D * 4), flat(h0, ns),
+                   rows_of(dout, a.rows, a.ld_out, D, a.bf16), flat(dh_T, ns), flat(a.cu, a.cu ? 4LL * (a.S + 1) : 0)}))
+        return KDA_ERR_ARG;
     if (need > 0 && (!o.workspace || o.workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     a.u = u; a.dt = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.Dskip = Dskip; a.z = z; a.dt_bias = dt_bias;
     a.h0 = h0; a.dout = dout; a.dh_T = dh_T; a.du = du; a.ddt = ddt; a.dA = dA; a.dB = dB; a.dC = dC;
@@ -318,7 +363,7 @@ int kda_ssm_scan_bwd(const void *u, const void *dt, const float *A, const void *
         if (e == cudaSuccess) e = zero_f32(ddt_bias, ddt_bias ? a.D : 0, stream);
     }
     if (e == cudaSuccess && a.cu && dims->zero_rest && a.rows > 0) {
-        const long long es = a.bf16 ? 2 : 4, row = a.D * es, bc = (long long)a.G * a.N * es;
+        const long long row = a.D * es, bc = (long long)a.G * a.N * es;
         ZeroRest zr = {{du, ddt, dB, dC, dz}, {row, row, bc, bc, row}, {row, row, bc, bc, row}, dz ? 5 : 4};
         m.mark(stream);
         e = launch_zero_rest(zr, a.cu, a.S, a.T, stream);
@@ -339,7 +384,13 @@ int kda_ssm_step(const void *u, const void *dt, const float *A, const void *Bm, 
     if (!all_aligned({A, Dskip, dt_bias, h, h_out}) ||
         !rows_aligned(a.bf16, {u, dt, Bm, Cm, z, out}))
         return KDA_ERR_ALIGN;
-    if (!distinct({out, h_out}, {u, dt, A, Bm, Cm, Dskip, z, dt_bias}) || out == h) return KDA_ERR_ARG;
+    const long long D = a.D, bc = (long long)a.G * a.N, ns = (long long)a.S * D * a.N * 4;
+    const Mem mo = rows_of(out, a.rows, a.ld_out, D, a.bf16), ho = flat(h_out, ns), hi = flat(h, ns);
+    if (!distinct({mo, ho}, {rows_of(u, a.rows, a.ld_u, D, a.bf16), rows_of(dt, a.rows, a.ld_dt, D, a.bf16), rows_of(z, a.rows, a.ld_z, D, a.bf16),
+                   rows_of(Bm, a.rows, a.ld_B, bc, a.bf16), rows_of(Cm, a.rows, a.ld_C, bc, a.bf16), flat(A, D * a.N * 4),
+                   flat(Dskip, D * 4), flat(dt_bias, D * 4)}) ||
+        overlap(mo, hi) || !same_or_apart(ho, hi))
+        return KDA_ERR_ARG;
     a.u = u; a.dt = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.Dskip = Dskip; a.z = z; a.dt_bias = dt_bias;
     a.h0 = h; a.h_T = h_out; a.out = out;
     LaunchMarks m = marks_of(o);
@@ -362,8 +413,13 @@ int kda_block_norm_fwd(const void *residual, const void *block, const void *gate
     if (!all_aligned({scale, w_post, w_pre, res_out, x}) ||
         !rows_aligned(a.bf16, {residual, block, gate}))
         return KDA_ERR_ALIGN;
-    if (!distinct({x, res_out}, {block, gate, scale, w_post, w_pre}) || x == residual) return KDA_ERR_ARG;
-    if (res_out == residual && block && a.ld_res != a.D) return KDA_ERR_ARG;
+    const long long D = a.D;
+    const Mem mr = rows_of(residual, a.rows, a.ld_res, D, a.bf16), mo = rows_of(res_out, a.rows, D, D, a.bf16),
+              mx = rows_of(x, a.rows, D, D, a.bf16);
+    if (!distinct({mx, mo}, {rows_of(block, a.rows, a.ld_block, D, a.bf16), rows_of(gate, a.rows, a.ld_gate, D, a.bf16),
+                             flat(scale, D * 4), flat(w_post, D * 4), flat(w_pre, D * 4)}) ||
+        overlap(mx, mr) || !same_or_apart(mo, mr))
+        return KDA_ERR_ARG;
     a.residual = residual; a.block = block; a.gate = gate; a.scale = scale; a.w_post = w_post; a.w_pre = w_pre;
     a.res_out = res_out; a.x = x;
     LaunchMarks m = marks_of(o);
@@ -396,11 +452,18 @@ int kda_block_norm_bwd(const void *res_out, const void *block, const void *gate,
     if (!all_aligned({scale, w_post, w_pre, dres, dx, dresidual, dblock, dgate, dscale, dw_post, dw_pre, o.workspace}) ||
         !rows_aligned(a.bf16, {res_out, block, gate}))
         return KDA_ERR_ALIGN;
-    if (!distinct({dresidual, dblock, dgate, dscale, dw_post, dw_pre, o.workspace},
-                  {res_out, block, gate, scale, w_post, w_pre, dx}))
-        return KDA_ERR_ARG;
-    if (dres && (dres == dblock || dres == dgate || dres == o.workspace)) return KDA_ERR_ARG;
     const size_t need = block_norm_bwd_workspace_bytes(a.rows, a.D);
+    const long long D = a.D, nd = (long long)a.rows * D * (a.bf16 ? 2 : 4);
+    const Mem md = flat(dresidual, nd), mi = flat(dres, nd), mb = flat(dblock, nd), mg = flat(dgate, nd),
+              mw = flat(o.workspace, (long long)need);
+    if (!distinct({md, mb, mg, flat(dscale, D * 4), flat(dw_post, D * 4), flat(dw_pre, D * 4), mw},
+                  {rows_of(res_out, a.rows, a.ld_res, D, a.bf16), rows_of(block, a.rows, a.ld_block, D, a.bf16),
+                   rows_of(gate, a.rows, a.ld_gate, D, a.bf16), flat(scale, D * 4), flat(w_post, D * 4), flat(w_pre, D * 4),
+                   flat(dx, nd)}))
+        return KDA_ERR_ARG;
+    if (!same_or_apart(md, mi) || overlap(mb, mi) || overlap(mg, mi) || overlap(mw, mi) || overlap(flat(dscale, D * 4), mi) ||
+        overlap(flat(dw_post, D * 4), mi) || overlap(flat(dw_pre, D * 4), mi))
+        return KDA_ERR_ARG;
     if (need > 0 && (!o.workspace || o.workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     a.residual = res_out; a.block = block; a.gate = gate; a.scale = scale; a.w_post = w_post; a.w_pre = w_pre;
     a.dres = dres; a.dx = dx; a.dresidual = dresidual; a.dblock = dblock; a.dgate = dgate;

@@ -41,6 +41,13 @@ struct FwdShape {
     static constexpr int BC = N / 4;                     // values of B and C a thread loads: 8 threads a token
 };
 
+// A log2(e), the exponent a unit of delta.  Finite where A is or is -inf: a token behind a span has
+// delta = 0 and has to leave the state as it is.
+__device__ __forceinline__ float rate(float a) {
+    const float r = a * kLog2e;
+    return r < -3.4028234e38f ? -3.4028234e38f : r;
+}
+
 // Sum of v[i] over the NQ lanes of a channel; lane q gets the sum of v[q].
 template <int NQ>
 __device__ __forceinline__ float reduce_states(float (&v)[NQ], int q) {

@@ -40,8 +40,8 @@ __global__ void __launch_bounds__(kFwdThreads, 3) ssm_bwd_sweep_kernel(const Ssm
 #pragma unroll
     for (int i = 0; i < P; i += 2) {
         const float4 v = *reinterpret_cast<const float4 *>(a.A + (long long)c * N + q * SPT + 2 * i);
-        A2[i] = make_float2(v.x * kLog2e, v.y * kLog2e);
-        A2[i + 1] = make_float2(v.z * kLog2e, v.w * kLog2e);
+        A2[i] = make_float2(rate(v.x), rate(v.y));
+        A2[i + 1] = make_float2(rate(v.z), rate(v.w));
         h[i] = h[i + 1] = G[i] = G[i + 1] = make_float2(0.f, 0.f);
         W[i] = W[i + 1] = make_float2(1.f, 1.f);
     }
@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(kBwdThreads, 3) ssm_bwd_kernel(const SsmP a) {
                 vh = order(*reinterpret_cast<const float4 *>(a.hst + (at + j) * N + 4 * q), p);
                 vg = order(*reinterpret_cast<const float4 *>(a.gst + (at + j) * N + 4 * q), p);
             }
-            A2[j][0] = make_float2(va.x * kLog2e, va.y * kLog2e);
-            A2[j][1] = make_float2(va.z * kLog2e, va.w * kLog2e);
+            A2[j][0] = make_float2(rate(va.x), rate(va.y));
+            A2[j][1] = make_float2(rate(va.z), rate(va.w));
             h[j][0] = make_float2(vh.x, vh.y);
             h[j][1] = make_float2(vh.z, vh.w);
             carry[j][0] = make_float2(vg.x, vg.y);

@@ -45,8 +45,8 @@ __global__ void __launch_bounds__(kFwdThreads, 4) ssm_fwd_kernel(const SsmP a) {
 #pragma unroll
         for (int i = 0; i < P; i += 2) {
             const float4 v = *reinterpret_cast<const float4 *>(a.A + (long long)c * N + q * SPT + 2 * i);
-            A2[i] = make_float2(v.x * kLog2e, v.y * kLog2e);
-            A2[i + 1] = make_float2(v.z * kLog2e, v.w * kLog2e);
+            A2[i] = make_float2(rate(v.x), rate(v.y));
+            A2[i + 1] = make_float2(rate(v.z), rate(v.w));
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
             if (src) s = *reinterpret_cast<const float4 *>(src + q * SPT + 2 * i);
             h[i] = make_float2(s.x, s.y);
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(SeqShape<T, N>::THREADS, 2) ssm_seq_kernel(con
         const float *src = a.h0 ? a.h0 + ((long long)b.sp.seq * a.D + c) * N : nullptr;
 #pragma unroll
         for (int i = 0; i < SPT; ++i) {
-            A2[i] *= kLog2e;
+            A2[i] = rate(A2[i]);
             h[i] = 0.f;
         }
         if (src) load_f32<float, SPT>(src + q * SPT, h);
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(128) ssm_seams_kernel(const SsmP a, int N) {
     float A2[4], v[4] = {0.f, 0.f, 0.f, 0.f};
     load_f32<float, 4>(a.A + e, A2);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) A2[i] *= kLog2e;
+    for (int i = 0; i < 4; ++i) A2[i] = rate(A2[i]);
     const float *from = back ? a.dh_T : a.h0;
     if (from) load_f32<float, 4>(from + s * all + e, v);
     float *seam = back ? a.gst : a.hst;
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(128) ssm_step_kernel(const SsmP a, int per) {
     load_f32<float, 4>(a.A + (long long)c * N + 4 * q, A);
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.Dskip ? a.Dskip[c] : 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) A[i] *= kLog2e;
+    for (int i = 0; i < 4; ++i) A[i] = rate(A[i]);
     for (; s < s1; s += R) {
         In x[R];
 #pragma unroll

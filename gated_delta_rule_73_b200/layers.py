@@ -8,11 +8,14 @@ with torch and return them.  Sequences are dense (``x [B, T, D]``) or packed (``
 for packed sequences hold zeros in rows of no sequence; outputs that are passed in keep theirs.
 
 All tensors of a call live on one device; work goes to ``stream`` or to that device's current one,
-whichever device is current in the calling thread.
+whichever device is current in the calling thread.  What the functions without the prefix allocate
+belongs to that stream: use it there, or order other streams behind it and tell the allocator
+(``Tensor.record_stream``).
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -173,14 +176,20 @@ def _launch(fn, call, args, dims, opts, stream):
         raise KdaError(fn.__name__, st)
 
 
-def _workspace(nbytes, device, stream):
-    """Scratch for one call, from the memory of the stream that uses it."""
-    if nbytes == 0:
-        return None
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+def _on_stream(f):
+    """What f allocates comes from the memory of the stream that it is given."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, stream=stream, **kw)
+    return call
+
+
+def _workspace(nbytes, device):
+    """Scratch for one call."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 def _rows_like(x):
@@ -272,6 +281,7 @@ def kda_short_conv_step(x, w, bias, state, state_out, y, *, silu=True, stream=No
     _launch(_lib.kda_short_conv_step, call, args, d, _opts(x.dtype), stream)
 
 
+@_on_stream
 def short_conv_fwd(x, w, bias=None, state0=None, *, cu_seqlens=None, silu=True, y=None, stream=None):
     """Causal depthwise convolution with SiLU; returns (y, state_T)."""
     zero = y is None and cu_seqlens is not None
@@ -283,11 +293,12 @@ def short_conv_fwd(x, w, bias=None, state0=None, *, cu_seqlens=None, silu=True, 
     return y, state_T
 
 
+@_on_stream
 def short_conv_bwd(x, w, bias, state0, dy, dstate_T=None, *, cu_seqlens=None, silu=True, workspace=None,
                    stream=None):
     """Gradients of ``short_conv_fwd``; returns (dx, dw, dbias, dstate0), None for what was not passed."""
     if workspace is None:
-        workspace = _workspace(kda_short_conv_bwd_workspace_bytes(x, w, cu_seqlens=cu_seqlens), x.device, stream)
+        workspace = _workspace(kda_short_conv_bwd_workspace_bytes(x, w, cu_seqlens=cu_seqlens), x.device)
     e = lambda t, dtype=_F32: None if t is None else torch.empty(t.shape, dtype=dtype, device=x.device)  # noqa: E731
     dx, dw, dbias, dstate0 = e(x, x.dtype), e(w), e(bias), e(state0)
     kda_short_conv_bwd(x, w, bias, state0, dy, dstate_T, dx, dw, dbias, dstate0, workspace, cu_seqlens=cu_seqlens,
@@ -295,6 +306,7 @@ def short_conv_bwd(x, w, bias, state0, dy, dstate_T=None, *, cu_seqlens=None, si
     return dx, dw, dbias, dstate0
 
 
+@_on_stream
 def short_conv_step(x, w, bias, state, *, state_out=None, silu=True, y=None, stream=None):
     """One row a sequence; state is updated in place unless state_out is given.  Returns y."""
     if y is None:
@@ -380,11 +392,12 @@ def kda_ssm_step(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h, h_out, out, *, dt_softp
     _launch(_lib.kda_ssm_step, call, args + (call.flat(h_out, "h_out", state, _F32), po), d, _opts(u.dtype), stream)
 
 
+@_on_stream
 def ssm_scan_fwd(u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, h0=None, *, cu_seqlens=None, dt_softplus=True,
                  out=None, workspace=None, stream=None):
     """Selective scan over sequences; returns (out, h_T)."""
     if workspace is None:
-        workspace = _workspace(kda_ssm_scan_fwd_workspace_bytes(u, A, Bm, cu_seqlens=cu_seqlens), u.device, stream)
+        workspace = _workspace(kda_ssm_scan_fwd_workspace_bytes(u, A, Bm, cu_seqlens=cu_seqlens), u.device)
     zero = out is None and cu_seqlens is not None
     if out is None:
         out = _rows_like(u)
@@ -395,12 +408,13 @@ def ssm_scan_fwd(u, dt, A, Bm, Cm, Dskip=None, z=None, dt_bias=None, h0=None, *,
     return out, h_T
 
 
+@_on_stream
 def ssm_scan_bwd(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, dout, dh_T=None, *, cu_seqlens=None, dt_softplus=True,
                  workspace=None, stream=None):
     """Gradients of ``ssm_scan_fwd``; returns (du, ddt, dA, dB, dC, dDskip, dz, ddt_bias, dh0), None for
     what was not passed."""
     if workspace is None:
-        workspace = _workspace(kda_ssm_scan_bwd_workspace_bytes(u, A, Bm, cu_seqlens=cu_seqlens), u.device, stream)
+        workspace = _workspace(kda_ssm_scan_bwd_workspace_bytes(u, A, Bm, cu_seqlens=cu_seqlens), u.device)
     e = lambda t, dtype: None if t is None else torch.empty(t.shape, dtype=dtype, device=u.device)  # noqa: E731
     g = (e(u, u.dtype), e(u, u.dtype), e(A, _F32), e(Bm, u.dtype), e(Bm, u.dtype), e(Dskip, _F32), e(z, u.dtype),
          e(dt_bias, _F32), e(h0, _F32))
@@ -409,6 +423,7 @@ def ssm_scan_bwd(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, dout, dh_T=None, *, cu
     return g
 
 
+@_on_stream
 def ssm_step(u, dt, A, Bm, Cm, Dskip, z, dt_bias, h, *, h_out=None, dt_softplus=True, out=None, stream=None):
     """One token a sequence; h is updated in place unless h_out is given.  Returns out."""
     if out is None:
@@ -464,6 +479,7 @@ def kda_block_norm_bwd(res_out, block, gate, scale, w_post, w_pre, dres, dx, dre
     _launch(_lib.kda_block_norm_bwd, call, args, d, _opts(res_out.dtype, workspace, call.device), stream)
 
 
+@_on_stream
 def block_norm_fwd(residual, block=None, gate=None, scale=None, w_post=None, w_pre=None, *, eps=1e-5,
                    want_x=True, stream=None):
     """Norms behind a block and ahead of the next; returns (res_out, x), None for what is not computed."""
@@ -473,11 +489,12 @@ def block_norm_fwd(residual, block=None, gate=None, scale=None, w_post=None, w_p
     return res_out, x
 
 
+@_on_stream
 def block_norm_bwd(res_out, block, gate, scale, w_post, w_pre, dres, dx, *, eps=1e-5, workspace=None, stream=None):
     """Gradients of ``block_norm_fwd``; returns (dresidual, dblock, dgate, dscale, dw_post, dw_pre), None for
     what was not passed."""
     if workspace is None:
-        workspace = _workspace(kda_block_norm_bwd_workspace_bytes(res_out), res_out.device, stream)
+        workspace = _workspace(kda_block_norm_bwd_workspace_bytes(res_out), res_out.device)
     e = lambda t, dtype: None if t is None else torch.empty(t.shape, dtype=dtype, device=res_out.device)  # noqa: E731
     g = (e(res_out, res_out.dtype), e(block, res_out.dtype), e(gate, res_out.dtype), e(scale, _F32), e(w_post, _F32),
          e(w_pre, _F32))

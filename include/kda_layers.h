@@ -23,8 +23,8 @@
  * At most 2^31 - 256 rows.  Row strides (ld_*) count elements, at most 2^27; 0 means the
  * row's own length (contiguous).  A tensor with a row stride may so be a column range of a
  * wider one, and unlike the others it may start at any element; rows at 16 bytes are read in
- * wider accesses.  Inputs and outputs must not overlap unless a comment says so; where
- * pointers show it, the call is refused (KDA_ERR_ARG).
+ * wider accesses.  Outputs must not overlap inputs or each other unless a comment says so
+ * (KDA_ERR_ARG); column ranges of one wider tensor do not.
  *
  * Gradients of activations have the activation type, gradients of parameters and states
  * are FP32; all are written, not accumulated, and every sum has a fixed order.

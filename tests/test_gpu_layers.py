@@ -287,6 +287,55 @@ def test_ssm_step_continues_the_sequence(K, D, N, G, dtype):
     R.check("h", h, rh, fh, 24 * T + 64)
 
 
+@pytest.mark.parametrize("dtype", DT)
+def test_empty_calls(K, dtype):
+    """No tokens: states go through; no sequences or no channels: sums of nothing."""
+    e = lambda *s, t=dtype: torch.randn(*s, device="cuda").to(t)  # noqa: E731
+    for B, T, D in ((3, 0, 16), (0, 5, 16), (2, 4, 0), (0, 0, 0)):
+        x, w, b, s0 = e(B, T, D), e(D, 4), e(D), e(B, 3, D)
+        y, sT = K.short_conv_fwd(x, w, b, s0)
+        assert y.shape == x.shape and sT.shape == s0.shape
+        g = e(B, 3, D, t=torch.float32)
+        dx, dw, db, ds = K.short_conv_bwd(x, w, b, s0, e(B, T, D), g)
+        A, Bm, Cm = -torch.rand(D, 8, device="cuda"), e(B, T, 1, 8), e(B, T, 1, 8)
+        Ds, bias, h0 = e(D, t=torch.float32), e(D, t=torch.float32), e(B, D, 8, t=torch.float32)
+        out, hT = K.ssm_scan_fwd(x, x.clone(), A, Bm, Cm, Ds, x.clone(), bias, h0)
+        gh = torch.randn_like(h0)
+        got = K.ssm_scan_bwd(x, x.clone(), A, Bm, Cm, Ds, x.clone(), bias, h0, e(B, T, D), gh)
+        if T == 0:
+            assert torch.equal(sT, s0) and torch.equal(ds, g) and torch.equal(hT, h0) and torch.equal(got[8], gh)
+        if B == 0 or T == 0:
+            assert (dw == 0).all() and (db == 0).all() and all((got[i] == 0).all() for i in (2, 5, 7))
+        if D > 0:
+            _, n = K.block_norm_fwd(x)
+            assert n.shape == x.shape
+
+
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+def test_ssm_state_behind_a_cut_tile(K, N):
+    """An infinite decay rate forgets everything at every token, and only there: the last state is the
+    last token's input whatever the sequence's length is to the tiles, forward and from gradients."""
+    g = _gen(N)
+    for T in (1, 5, 17, 33, 70):
+        u, dt = _n(g, 1, T, 40), _n(g, 1, T, 40)
+        Bm, Cm = _n(g, 1, T, 1, N), _n(g, 1, T, 1, N)
+        for A in (torch.full((40, N), -float("inf"), device="cuda"), torch.full((40, N), -3.4e38, device="cuda")):
+            h0 = _n(g, 1, 40, N)
+            out, hT = K.ssm_scan_fwd(u, dt, A, Bm, Cm, h0=h0)
+            d = torch.nn.functional.softplus(R.d(dt), threshold=100)
+            ref = (d * R.d(u))[..., None] * R.d(Bm)
+            R.check("h_T", hT, ref[:, -1], ref[:, -1].abs(), 48)
+            h = torch.empty_like(h0)
+            K.ssm_step(u[:, -1], dt[:, -1], A, Bm[:, -1], Cm[:, -1], None, None, None, h0, h_out=h)
+            R.check("step", h, ref[:, -1], ref[:, -1].abs(), 48)
+            dout = _n(g, 1, T, 40)
+            got = K.ssm_scan_bwd(u, dt, A, Bm, Cm, None, None, None, h0, dout, torch.zeros_like(h0))
+            dC = (R.d(dout)[..., None] * ref).sum(2, keepdim=True).squeeze(2)[:, :, None]
+            far = (R.d(dout)[..., None] * ref).abs().sum(2)[:, :, None]
+            R.check("dC", got[4], dC, far, 48 + 40)
+            assert (got[8] == 0).all()
+
+
 def test_ssm_extreme_steps(K):
     """delta of 0 keeps the state, a large delta forgets it; gates far out shut or pass."""
     B, T, D, N = 1, 70, 32, 16

@@ -21,7 +21,7 @@ def L():
 
 def _call(L, name, n, dims, opts=None, null=(), at=(), same=()):
     """Status of a call whose n pointers are all good ones, but for `null`, `at` (index, address), `same` (i, j)."""
-    p = [0x10000 * (i + 1) for i in range(n)]
+    p = [(i + 1) << 28 for i in range(n)]
     for i in null:
         p[i] = None
     for i, a in at:
@@ -63,21 +63,26 @@ def test_short_conv_refusals(L):
     for i in (0, 1, 4):
         assert fwd(_conv(L), null=[i]) == ARG
     for i in range(6):   # rows may start at any element, the others at 16 bytes
-        assert fwd(_conv(L), at=[(i, 0x10008 if i not in (0, 4) else 0x10001)]) == ALIGN
+        assert fwd(_conv(L), at=[(i, (i + 1 << 28) + (8 if i not in (0, 4) else 1))]) == ALIGN
     assert fwd(_conv(L), same=[(4, 0)]) == ARG and fwd(_conv(L), same=[(5, 3)]) == ARG
     assert fwd(_conv(L), opts=_opts(L, flags=2)) == ARG      # a flag of the delta rule
     assert fwd(_conv(L), opts=_opts(L, dtype=5)) == ARG
     assert fwd(None) == ARG
     assert fwd(_conv(L, B=0)) == 0 and fwd(_conv(L, D=0)) == 0
+    assert fwd(_conv(L, cu_seqlens=(1 << 28) + 2)) == ALIGN
+    # y a row behind x, inside it; beside it in wider rows (refused for its alignment alone, behind the overlap's check)
+    assert fwd(_conv(L), at=[(4, (1 << 28) + 32)]) == ARG
+    assert fwd(_conv(L, ld_x=32, ld_y=32), at=[(4, (1 << 28) + 16)]) == ARG
+    assert fwd(_conv(L, ld_x=32, ld_y=33), at=[(4, (1 << 28) + 32)]) == ARG
     bwd = lambda d, **kw: _call(L, "kda_short_conv_bwd", 10, d, **kw)  # noqa: E731
     need = L._lib.kda_short_conv_bwd_workspace_bytes(_conv(L), None)
     assert need > 0
     assert bwd(_conv(L)) == WORKSPACE
-    assert bwd(_conv(L), opts=_opts(L, 0x900000, need - 1)) == WORKSPACE
-    assert bwd(_conv(L), opts=_opts(L, 0x900008, need)) == ALIGN
-    assert bwd(_conv(L), opts=_opts(L, 0x10000, need)) == ARG    # the workspace is an input
+    assert bwd(_conv(L), opts=_opts(L, 1 << 40, need - 1)) == WORKSPACE
+    assert bwd(_conv(L), opts=_opts(L, (1 << 40) + 8, need)) == ALIGN
+    assert bwd(_conv(L), opts=_opts(L, 1 << 28, need)) == ARG    # the workspace is an input
     for i in (0, 1, 4, 6, 7):
-        assert bwd(_conv(L), null=[i], opts=_opts(L, 0x900000, need)) == ARG
+        assert bwd(_conv(L), null=[i], opts=_opts(L, 1 << 40, need)) == ARG
     step = lambda d, **kw: _call(L, "kda_short_conv_step", 6, d, **kw)  # noqa: E731
     for i in (0, 1, 3, 4, 5):
         assert step(_conv(L), null=[i]) == ARG
@@ -94,16 +99,16 @@ def test_ssm_refusals(L):
     for i in (0, 1, 2, 3, 4, 9):
         assert fwd(_ssm(L), null=[i]) == ARG
     for i in range(11):
-        assert fwd(_ssm(L), at=[(i, 0x10008 if i not in (0, 1, 3, 4, 6, 9) else 0x10001)]) == ALIGN
+        assert fwd(_ssm(L), at=[(i, (i + 1 << 28) + (8 if i not in (0, 1, 3, 4, 6, 9) else 1))]) == ALIGN
     assert fwd(_ssm(L), same=[(10, 8)]) == ARG      # h_T over h0
     long = _ssm(L, T=4096)
     need = L._lib.kda_ssm_scan_fwd_workspace_bytes(long, None)
     assert need > 0 and fwd(long) == WORKSPACE
-    assert fwd(long, opts=_opts(L, 0x900000, need - 4)) == WORKSPACE
+    assert fwd(long, opts=_opts(L, 1 << 40, need - 4)) == WORKSPACE
     bwd = lambda d, **kw: _call(L, "kda_ssm_scan_bwd", 20, d, **kw)  # noqa: E731
     need = L._lib.kda_ssm_scan_bwd_workspace_bytes(_ssm(L), None)
-    assert bwd(_ssm(L)) == WORKSPACE and bwd(_ssm(L), opts=_opts(L, 0x900000, need - 1)) == WORKSPACE
-    ok = _opts(L, 0x900000, need)
+    assert bwd(_ssm(L)) == WORKSPACE and bwd(_ssm(L), opts=_opts(L, 1 << 40, need - 1)) == WORKSPACE
+    ok = _opts(L, 1 << 40, need)
     for i in (0, 1, 2, 3, 4, 9, 11, 12, 13, 14, 15):
         assert bwd(_ssm(L), null=[i], opts=ok) == ARG
     assert bwd(_ssm(L), null=[6], opts=ok) == ARG and bwd(_ssm(L), null=[17], opts=ok) == ARG   # z without dz, dz without z
@@ -112,6 +117,7 @@ def test_ssm_refusals(L):
     for i in (0, 1, 2, 3, 4, 8, 9, 10):
         assert step(_ssm(L), null=[i]) == ARG
     assert step(_ssm(L), same=[(10, 8)]) == ARG
+    assert step(_ssm(L), at=[(9, (9 << 28) + 64)]) == ARG   # h_out inside h, not in place
     assert step(_ssm(L, B=0)) == 0
 
 
@@ -129,7 +135,7 @@ def test_norm_refusals(L):
     bwd = lambda d, **kw: _call(L, "kda_block_norm_bwd", 14, d, **kw)  # noqa: E731
     need = L._lib.kda_block_norm_bwd_workspace_bytes(_norm(L), None)
     assert bwd(_norm(L)) == WORKSPACE
-    ok = _opts(L, 0x900000, need)
+    ok = _opts(L, 1 << 40, need)
     assert bwd(_norm(L), null=[6, 7], opts=ok) == ARG
     for i in (0, 1, 2, 8, 9, 10):   # also a block without dblock, a gate without dgate and the other way round
         assert bwd(_norm(L), null=[i], opts=ok) == ARG
@@ -148,6 +154,21 @@ def test_binding_refuses_what_the_library_could_not_see(L):
         L.short_conv_fwd(x[0], w)                                  # rows without cu_seqlens
     with pytest.raises(TypeError):
         L.short_conv_fwd(x[0], w, cu_seqlens=torch.tensor([0, 4]))  # int64
+
+
+def test_column_ranges_do_not_overlap(L):
+    """What the C side calls an overlap, on calls that end at a later check (no workspace)."""
+    d = _conv(L, ld_x=32, ld_y=32, ld_dx=48)
+    bwd = lambda at, d=d: _call(L, "kda_short_conv_bwd", 10, d, at=at)  # noqa: E731
+    if torch.cuda.is_available():
+        pytest.skip("made-up device addresses")
+    assert bwd([(4, (1 << 28) + 32)]) == WORKSPACE            # x and dy side by side: both inputs anyway
+    assert bwd([(6, (1 << 28) + 32)]) == ARG                  # dx in rows 48 apart over x in rows 32 apart
+    e = _conv(L, ld_x=48, ld_y=48, ld_dx=48)
+    assert bwd([(6, (1 << 28) + 32)], e) == WORKSPACE         # columns 16 .. 31 of rows of 48
+    assert bwd([(6, (1 << 28) + 64)], e) == WORKSPACE         # 32 .. 47
+    assert bwd([(6, (1 << 28) + 80)], e) == ARG               # 40 .. 55: over the next row's first
+    assert bwd([(6, (1 << 28) - 32)], e) == WORKSPACE and bwd([(6, (1 << 28) - 16)], e) == ARG
 
 
 def test_row_strides_of_views(L):
