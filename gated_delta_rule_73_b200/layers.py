@@ -96,13 +96,10 @@ class _Call:
         """(address, row stride) of a row tensor [*lead, *tail]; (None, 0) for None."""
         if t is None:
             return None, 0
-        shape = self.lead + tail
-        if not (isinstance(t, torch.Tensor) and t.dtype is self.dtype and t.shape == shape
+        if not (isinstance(t, torch.Tensor) and t.dtype is self.dtype and t.shape == self.lead + tail
                 and t.get_device() == self.device):
-            self._refuse(t, name, shape, self.dtype)
-        if t.is_contiguous():
-            return t.data_ptr(), 0
-        return t.data_ptr(), self._row_stride(t.stride(), name, tail)
+            self._refuse(t, name, self.lead + tail, self.dtype)
+        return t.data_ptr(), 0 if t.is_contiguous() else self._row_stride(t.stride(), name, tail)
 
     def _refuse(self, t, name, shape, dtype):
         if not isinstance(t, torch.Tensor):
@@ -212,10 +209,7 @@ def _sequences(x, cu_seqlens):
     return lead, cu_seqlens.shape[0] - 1, lead[0]
 
 
-def _sizes(*sizes):
-    """The C structures hold sizes as int."""
-    if max(sizes) > 0x7fffffff:
-        raise ValueError(f"sizes {sizes} do not fit an int")
+_INT = 0x7fffffff   # the C structures hold sizes as int
 
 
 def _cu(call, cu_seqlens):
@@ -228,15 +222,18 @@ def _conv_call(x, w, cu_seqlens, silu, zero_rest, step=False):
         raise TypeError("x and w must be torch.Tensors")
     if w.dim() != 2:
         raise ValueError(f"w has shape {tuple(w.shape)}, expected [D, K]")
+    shape = x.shape
     if step:
-        if x.dim() != 2:
-            raise ValueError(f"x has shape {tuple(x.shape)}, expected [B, D]")
-        lead, B, T = x.shape[:1], x.shape[0], 1
+        if len(shape) != 2:
+            raise ValueError(f"x has shape {tuple(shape)}, expected [B, D]")
+        B, T = shape[0], 1
+        lead = (B,)
     else:
         lead, B, T = _sequences(x, cu_seqlens)
     call = _Call(x, "x", lead)
-    D, K = x.shape[-1], w.shape[1]
-    _sizes(B, T, D, K)
+    D, K = shape[-1], w.shape[1]
+    if B | T | D | K > _INT:
+        raise ValueError(f"sizes {(B, T, D, K)} do not fit an int")
     d = kda_conv_dims(B=B, T=T, D=D, K=K, silu=1 if silu else 0, cu_seqlens=_cu(call, cu_seqlens), zero_rest=1 if zero_rest else 0)
     return call, d, (B, K - 1, D), (D, K)
 
@@ -274,9 +271,10 @@ def kda_short_conv_bwd(x, w, bias, state0, dy, dstate_T, dx, dw, dbias, dstate0,
 def kda_short_conv_step(x, w, bias, state, state_out, y, *, silu=True, stream=None) -> None:
     """Call ``kda_short_conv_step``; x, y [B,D], state, state_out [B,K-1,D] (state_out may be state)."""
     call, d, shape, taps = _conv_call(x, w, None, silu, False, step=True)
-    px, d.ld_x = call.rows(x, "x", (d.D,))
-    py, d.ld_y = call.rows(y, "y", (d.D,))
-    args = (px, call.flat(w, "w", taps), call.flat(bias, "bias", (d.D,)), call.flat(state, "state", shape),
+    row = taps[:1]
+    px, d.ld_x = call.rows(x, "x", row)
+    py, d.ld_y = call.rows(y, "y", row)
+    args = (px, call.flat(w, "w", taps), call.flat(bias, "bias", row), call.flat(state, "state", shape),
             call.flat(state_out, "state_out", shape), py)
     _launch(_lib.kda_short_conv_step, call, args, d, _opts(x.dtype), stream)
 
@@ -288,7 +286,7 @@ def short_conv_fwd(x, w, bias=None, state0=None, *, cu_seqlens=None, silu=True, 
     if y is None:
         y = _rows_like(x)
     B = x.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    state_T = torch.empty((B, w.shape[1] - 1, x.shape[-1]), dtype=x.dtype, device=x.device)
+    state_T = x.new_empty((B, w.shape[1] - 1, x.shape[-1]))
     kda_short_conv_fwd(x, w, bias, state0, y, state_T, cu_seqlens=cu_seqlens, silu=silu, zero_rest=zero, stream=stream)
     return y, state_T
 
@@ -317,35 +315,40 @@ def short_conv_step(x, w, bias, state, *, state_out=None, silu=True, y=None, str
 
 # ------------------------------------------------------------------ selective scan
 def _ssm_call(u, A, Bm, cu_seqlens, dt_softplus, zero_rest, step=False):
-    for t, name in ((u, "u"), (A, "A"), (Bm, "Bm")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
+    if not (isinstance(u, torch.Tensor) and isinstance(A, torch.Tensor) and isinstance(Bm, torch.Tensor)):
+        raise TypeError("u, A and Bm must be torch.Tensors")
     if A.dim() != 2:
         raise ValueError(f"A has shape {tuple(A.shape)}, expected [D, N]")
+    shape, groups = u.shape, Bm.shape
     if step:
-        if u.dim() != 2:
-            raise ValueError(f"u has shape {tuple(u.shape)}, expected [B, D]")
-        lead, B, T = u.shape[:1], u.shape[0], 1
+        if len(shape) != 2:
+            raise ValueError(f"u has shape {tuple(shape)}, expected [B, D]")
+        B, T = shape[0], 1
+        lead = (B,)
     else:
         lead, B, T = _sequences(u, cu_seqlens)
-    if Bm.dim() != len(lead) + 2:
-        raise ValueError(f"Bm has shape {tuple(Bm.shape)}, expected {tuple(lead)} + [G, N]")
+    if len(groups) != len(lead) + 2:
+        raise ValueError(f"Bm has shape {tuple(groups)}, expected {tuple(lead)} + [G, N]")
     call = _Call(u, "u", lead)
-    D, N, G = u.shape[-1], A.shape[1], Bm.shape[-2]
-    _sizes(B, T, D, N, G)
+    D, N, G = shape[-1], A.shape[1], groups[-2]
+    if B | T | D | N | G > _INT:
+        raise ValueError(f"sizes {(B, T, D, N, G)} do not fit an int")
     d = kda_ssm_dims(B=B, T=T, D=D, N=N, G=G, dt_softplus=1 if dt_softplus else 0, cu_seqlens=_cu(call, cu_seqlens),
                      zero_rest=1 if zero_rest else 0)
     return call, d, (B, D, N)
 
 
 def _ssm_inputs(call, d, u, dt, A, Bm, Cm, Dskip, z, dt_bias, h0, state):
-    pu, d.ld_u = call.rows(u, "u", (d.D,))
-    pdt, d.ld_dt = call.rows(dt, "dt", (d.D,))
-    pz, d.ld_z = call.rows(z, "z", (d.D,))
-    pB, d.ld_B = call.rows(Bm, "Bm", (d.G, d.N))
-    pC, d.ld_C = call.rows(Cm, "Cm", (d.G, d.N))
-    return (pu, pdt, call.flat(A, "A", (d.D, d.N), _F32), pB, pC, call.flat(Dskip, "Dskip", (d.D,), _F32), pz,
-            call.flat(dt_bias, "dt_bias", (d.D,), _F32), call.flat(h0, "h0", state, _F32))
+    rates = state[1:]                     # (D, N)
+    row, bc = rates[:1], (d.G, rates[1])
+    rows, flat = call.rows, call.flat
+    pu, d.ld_u = rows(u, "u", row)
+    pdt, d.ld_dt = rows(dt, "dt", row)
+    pz, d.ld_z = rows(z, "z", row)
+    pB, d.ld_B = rows(Bm, "Bm", bc)
+    pC, d.ld_C = rows(Cm, "Cm", bc)
+    return (pu, pdt, flat(A, "A", rates, _F32), pB, pC, flat(Dskip, "Dskip", row, _F32), pz,
+            flat(dt_bias, "dt_bias", row, _F32), flat(h0, "h0", state, _F32))
 
 
 def kda_ssm_scan_fwd_workspace_bytes(u, A, Bm, *, cu_seqlens=None) -> int:
@@ -441,7 +444,8 @@ def _norm_call(residual, name, eps):
         raise ValueError(f"{name} must be [..., D]")
     lead, D = residual.shape[:-1], residual.shape[-1]
     rows = math.prod(lead)
-    _sizes(rows, D)
+    if rows | D > _INT:
+        raise ValueError(f"sizes {(rows, D)} do not fit an int")
     return _Call(residual, name, lead), kda_norm_dims(rows=rows, D=D, eps=eps)
 
 
