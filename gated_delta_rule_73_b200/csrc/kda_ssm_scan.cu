@@ -444,70 +444,78 @@ __global__ void __launch_bounds__(128) ssm_seams_kernel(const SsmP a, int N) {
 }
 
 // One token: bound by the states' bytes, read and written once.  A lane holds four states of a channel,
-// its parameters with them, and walks sequences, two at a time, the next two's loads under way.
-template <typename T, int N>
+// its parameters with them, and walks sequences, R at a time, the next R's loads under way.  What a
+// sequence and channel has once (delta, the gate) is worked out by one lane (of each R) and handed round.
+template <typename T, int N, int R>
 __global__ void __launch_bounds__(128) ssm_step_kernel(const SsmP a, int per) {
-    constexpr int NQ = N / 4, R = 2;
-    const int unit = blockIdx.x * (128 / NQ) + threadIdx.x / NQ, q = threadIdx.x % NQ;
+    constexpr int NQ = N / 4;
+    static_assert(R <= NQ, "a lane for each sequence");
+    const int unit = blockIdx.x * (128 / NQ) + threadIdx.x / NQ, q = threadIdx.x % NQ, own = q % R;
     const bool live = unit < a.D;                        // lanes of a channel agree
     const int c = live ? unit : 0, g = c / a.Dg;
     const int s1 = (blockIdx.y + 1) * per < a.q.S ? (blockIdx.y + 1) * per : a.q.S;
-    struct In {
-        float h[4];
-        Raw<T, 4> B, C;
-        T u, dt, z;
-    } next[R];
-    auto fetch = [&](In &x, int s) {                     // past the last: the last again, not stored
-        const long long r = s < s1 ? s : s1 - 1;
-        load_f32<float, 4>(a.h0 + (r * a.D + c) * N + 4 * q, x.h);
-        const T *pb = (const T *)a.Bm + r * a.ld_B + g * N + 4 * q, *pc = (const T *)a.Cm + r * a.ld_C + g * N + 4 * q;
-        x.B = a.vecb ? load_raw<T, 4>(pb) : load_part<T, 4>(pb, 4);
-        x.C = a.vecb ? load_raw<T, 4>(pc) : load_part<T, 4>(pc, 4);
-        x.u = ((const T *)a.u)[r * a.ld_u + c];
-        x.dt = ((const T *)a.dt)[r * a.ld_dt + c];
-        if (a.z) x.z = ((const T *)a.z)[r * a.ld_z + c];
+    float nh[R][4];
+    Raw<T, 4> nB[R], nC[R];
+    T nu, ndt, nz;
+    const T *pB = (const T *)a.Bm + g * N + 4 * q, *pC = (const T *)a.Cm + g * N + 4 * q;
+    const float *ph = a.h0 + (long long)c * N + 4 * q;
+    const long long hs = (long long)a.D * N;             // states of a sequence
+    auto fetch = [&](int s) {                            // past the last: the last again, not stored
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const long long t = s + r < s1 ? s + r : s1 - 1;
+            load_f32<float, 4>(ph + t * hs, nh[r]);
+            nB[r] = a.vecb ? load_raw<T, 4>(pB + t * a.ld_B) : load_part<T, 4>(pB + t * a.ld_B, 4);
+            nC[r] = a.vecb ? load_raw<T, 4>(pC + t * a.ld_C) : load_part<T, 4>(pC + t * a.ld_C, 4);
+        }
+        const long long t = s + own < s1 ? s + own : s1 - 1;
+        nu = ((const T *)a.u)[t * a.ld_u + c];
+        ndt = ((const T *)a.dt)[t * a.ld_dt + c];
+        if (a.z) nz = ((const T *)a.z)[t * a.ld_z + c];
     };
     int s = blockIdx.y * per;
     if (s >= s1) return;
-#pragma unroll
-    for (int r = 0; r < R; ++r) fetch(next[r], s + r);
+    fetch(s);
     float A[4];
     load_f32<float, 4>(a.A + (long long)c * N + 4 * q, A);
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.Dskip ? a.Dskip[c] : 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) A[i] = rate(A[i]);
     for (; s < s1; s += R) {
-        In x[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = next[r];
-        if (s + R < s1)
-#pragma unroll
-            for (int r = 0; r < R; ++r) fetch(next[r], s + R + r);
+        float h[R][4], y[R];
+        Raw<T, 4> B[R], C[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float bv[4], cv[4], y = 0.f;
-            widen<T, 4>(x[r].B, bv);
-            widen<T, 4>(x[r].C, cv);
-            const float u = to_f32(x[r].u);
-            float d = to_f32(x[r].dt) + bias;
-            if (a.softplus) d = softplus_f32(d);
+            B[r] = nB[r];
+            C[r] = nC[r];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[r][i] = nh[r][i];
+        }
+        const float u = to_f32(nu), z = a.z ? to_f32(nz) : 0.f;
+        float d = to_f32(ndt) + bias;
+        if (s + R < s1) fetch(s + R);
+        if (a.softplus) d = softplus_f32(d);
+        const float x = d * u;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float bv[4], cv[4];
+            widen<T, 4>(B[r], bv);
+            widen<T, 4>(C[r], cv);
+            const float dr = R > 1 ? __shfl_sync(0xffffffffu, d, r, NQ) : d;
+            const float xr = R > 1 ? __shfl_sync(0xffffffffu, x, r, NQ) : x;
+            y[r] = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[r].h[i] = fmaf(ex2(d * A[i]), x[r].h[i], d * u * bv[i]);
-                y = fmaf(cv[i], x[r].h[i], y);
+                h[r][i] = fmaf(ex2(dr * A[i]), h[r][i], xr * bv[i]);
+                y[r] = fmaf(cv[i], h[r][i], y[r]);
             }
 #pragma unroll
-            for (int o = NQ / 2; o >= 1; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-            if (live && s + r < s1) {
-                const long long t = s + r;
-                store_f32<float, 4>(a.h_T + (t * a.D + c) * N + 4 * q, x[r].h);
-                if (q == 0) {
-                    y = fmaf(skip, u, y);
-                    if (a.z) y *= silu_f32(to_f32(x[r].z));
-                    ((T *)a.out)[t * a.ld_out + c] = from_f32<T>(y);
-                }
-            }
+            for (int o = NQ / 2; o >= R; o >>= 1) y[r] += __shfl_xor_sync(0xffffffffu, y[r], o);
+            if (live && s + r < s1) store_f32<float, 4>(a.h_T + (s + r) * hs + (long long)c * N + 4 * q, h[r]);
         }
+        float o = fmaf(skip, u, reduce_states<R>(y, own));
+        if (a.z) o *= silu_f32(z);
+        if (live && q < R && s + own < s1) ((T *)a.out)[(long long)(s + own) * a.ld_out + c] = from_f32<T>(o);
     }
 }
 
@@ -578,16 +586,20 @@ cudaError_t run_fwd(const SsmArgs &a, cudaStream_t st) {
     ssm_fwd_kernel<T, N, false><<<(unsigned)blocks, kFwdThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
-// Blocks of 128 / (N / 4) channels, and as many parts of the sequences as make 4736 blocks (86 us for 256 x 12288 x 16 in
-// bf16, 89 with half as many, 97 with a lane for every two sequences).
+// Blocks of 128 / (N / 4) channels, and as many parts of the sequences as make 2368 blocks; four
+// sequences at a time where a part has them.  256 x 12288 x 16 in bf16: 80 us (83 with twice the
+// blocks); with every lane working out delta and the gate 85; a lane for each sequence, no walk, 115.
 template <typename T, int N>
 cudaError_t run_step(const SsmArgs &a, cudaStream_t st) {
     const SsmP p = ssm_params<1, 1, 4>(a, 1);
-    const int blocks = (a.D + 512 / N - 1) / (512 / N), parts = 4736 / blocks > 1 ? 4736 / blocks : 1;
+    constexpr int R = N == 8 ? 2 : 4;
+    const int blocks = (a.D + 512 / N - 1) / (512 / N), parts = 2368 / blocks > 1 ? 2368 / blocks : 1;
     const int per = (a.S + parts - 1) / parts, n = (a.S + per - 1) / per;
     if (n > 65535) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)blocks, (unsigned)n);
     a.marks->mark(st);
-    ssm_step_kernel<T, N><<<dim3((unsigned)blocks, (unsigned)n), 128, 0, st>>>(p, per);
+    if (per >= R) ssm_step_kernel<T, N, R><<<grid, 128, 0, st>>>(p, per);
+    else ssm_step_kernel<T, N, 1><<<grid, 128, 0, st>>>(p, per);
     return cudaGetLastError();
 }
 template <typename T>

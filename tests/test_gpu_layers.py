@@ -267,9 +267,11 @@ def test_ssm_scan_leaves_rows_of_no_sequence(K, dtype):
 
 
 @pytest.mark.parametrize("dtype", DT)
-@pytest.mark.parametrize("D,N,G", [(64, 16, 1), (33, 8, 3), (20, 64, 2), (130, 32, 1)])
-def test_ssm_step_continues_the_sequence(K, D, N, G, dtype):
-    B, T = 3, 6
+@pytest.mark.parametrize("B,D,N,G", [(3, 64, 16, 1), (3, 33, 8, 3), (3, 20, 64, 2), (3, 130, 32, 1),
+                                     # lanes walk several sequences: 9 in one part, parts of 3, 7 and 8, the last one shorter
+                                     (9, 75776, 16, 1), (11, 3 * 12600, 8, 3), (13, 9472, 64, 1), (22, 12000, 32, 2)])
+def test_ssm_step_continues_the_sequence(K, B, D, N, G, dtype):
+    T = 6 if B == 3 else 2
     args, _, bounds, _ = _ssm_inputs(_dense(B, T), D, N, G, True, True, True, True, 0, dtype)
     u, dt, A, Bm, Cm, Ds, z, bias, h0 = args
     (ro, rh), (fo, fh) = _ssm_ref(args, bounds), _ssm_ref(args, bounds, mag=True)
