@@ -87,7 +87,7 @@ cudaError_t launch_block_norm_fwd(const NormArgs &a, cudaStream_t st);
 cudaError_t launch_block_norm_bwd(const NormArgs &a, cudaStream_t st);
 
 // Zeroes the rows of a packed call that belong to no sequence: before cu[0], from cu[S] on.
-// Up to four outputs of `bytes[i]` a row, rows `pitch[i]` bytes apart.
+// Up to five outputs of `bytes[i]` a row, rows `pitch[i]` bytes apart.
 struct ZeroRest {
     void *p[5];
     long long bytes[5], pitch[5];

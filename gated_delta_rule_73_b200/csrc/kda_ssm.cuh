@@ -1,5 +1,5 @@
-// kda_ssm.cuh -- what the selective scan's forward and backward kernels share: the lanes'
-// layout, the loads of a tile of 16 tokens, the reductions between lanes.
+// kda_ssm.cuh -- what the selective scan's kernels share: arguments and the lanes' layouts, decay
+// rates, exponentials, the loads of a tile of B and C, the sums between lanes.
 #pragma once
 #include "kda_layers_internal.h"
 #include "kda_rows.cuh"

@@ -12,8 +12,10 @@
 // pass chains the spans.  The main kernel then walks its span forward once, keeping the state
 // every 8 tokens in shared memory, and goes back over windows of 4 tokens whose states and decay
 // factors stay in registers (the first four tokens of 8 are walked again for the second four):
-// 3.5 exponentials a state and token in all, no state in HBM but at the spans' seams.  It is bound
-// by issue slots: the products of the formulas above, on packed pairs, and the sums between lanes.
+// 3.4 exponentials a state and token in all, no state in HBM but at the spans' seams.  It is bound
+// by issue slots and latencies (31.5 instructions a state and token, 43 % of the slots, 11 warps an
+// SM): the products of the formulas above, on packed pairs, and the sums between lanes.  4096 tokens
+// x 2048 channels x 16 states in bf16: sweep 67 us, chain 8, main kernel 273, last sums 8.
 #include "kda_ssm.cuh"
 
 namespace kda {

@@ -14,7 +14,7 @@
 //    the special-function unit's rate.
 //  * whole sequences, four states a lane (ssm_seq_kernel): four times the lanes, and warps of their
 //    own for what surrounds the recurrence, so that a few thousand channels fill the device without
-//    a second pass over the exponentials: 307 us for 8192 x 4096 x 16, where the first takes 1780.
+//    a second pass over the exponentials: 302 us for 8192 x 4096 x 16, where the first takes 1780.
 //  * spans of time side by side (ssm_fwd_kernel twice): a span's effect on the state is
 //    h -> exp(A sum delta) h + (its end from zero), so one sweep finds the ends of all spans, a small
 //    pass chains them, and the spans then run side by side, for twice the exponentials: 82 us for
