@@ -15,7 +15,9 @@ struct SsmP {
     float *h_T, *dh0;
     Seqs q;
     int D, G, Dg, cpg, nblk;   // channels, groups, channels a group, channel blocks a group, in all
-    int softplus, vec, vecb;   // vec: channel vectors of u, dt, z, out aligned; vecb: B, C
+    bool vec, vecb;            // whole vectors: channels of u, dt, z, out, dout; values of B and C
+    bool vec_grad, vecb_sweep; // backward: channels of du, ddt, dz; B and C in the sweep
+    int softplus;
     int L;                     // rows a span
     long long ld_u, ld_dt, ld_z, ld_B, ld_C, ld_out, slots;
     // workspace: states and their gradients at the spans' seams [slots][D][N], the spans' sums of
@@ -71,7 +73,7 @@ __device__ __forceinline__ int spread(int c) { return c ^ ((c >> 3) & 7); }
 // The raw values of one tensor that a thread loads for its token and EPT channels.
 template <typename T, int EPT>
 __device__ __forceinline__ Raw<T, EPT> load_tile(const void *p, long long row, long long ld, int c, int left,
-                                                 bool ok, int vec) {
+                                                 bool ok, bool vec) {
     const T *a = (const T *)p + row * ld + c;
     if (ok && vec && left >= EPT) return load_raw<T, EPT>(a);
     return load_part<T, EPT>(a, ok ? left : 0);

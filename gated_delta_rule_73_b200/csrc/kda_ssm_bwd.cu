@@ -52,11 +52,10 @@ __global__ void __launch_bounds__(kFwdThreads, 3) ssm_bwd_sweep_kernel(const Ssm
     const T *pbc = bk < N ? (const T *)a.Bm + (b.sp.r0 + bt) * a.ld_B + b.g * N + bk
                           : (const T *)a.Cm + (b.sp.r0 + bt) * a.ld_C + b.g * N + bk - N;
     const long long ldbc = bk < N ? a.ld_B : a.ld_C;
-    const bool vecb = (a.vecb & 2) != 0;
     auto fetch_bc = [&](int t0) {
         const bool ok = t0 + bt < n;
         const T *p = pbc + t0 * ldbc;
-        return ok && vecb ? load_raw<T, BC>(p) : load_part<T, BC>(p, ok ? BC : 0);
+        return ok && a.vecb_sweep ? load_raw<T, BC>(p) : load_part<T, BC>(p, ok ? BC : 0);
     };
     auto put_bc = [&](const Raw<T, BC> &r, int buf) {
         float v[BC];
@@ -235,7 +234,6 @@ __global__ void __launch_bounds__(kBwdThreads, 3) ssm_bwd_kernel(const SsmP a) {
     const int lt = tid >> 4, lc = (tid & 15) * EPT;
     const int lleft = a.Dg - b.cin - lc;
     const int gc = b.g * a.Dg + b.cin + lc;
-    const bool vecb = (a.vecb & 1) != 0;
     float2 dA[2][2];
     float dD[EPT], dbias[EPT];
 #pragma unroll
@@ -273,10 +271,10 @@ __global__ void __launch_bounds__(kBwdThreads, 3) ssm_bwd_kernel(const SsmP a) {
         auto fetch_bc = [&](int t0, bool with_c) {
             const bool ok = bt < kStep && t0 + bt < n;
             const T *pb = (const T *)a.Bm + (b.sp.r0 + t0 + bt) * a.ld_B + b.g * N + bk;
-            rb = ok && vecb ? load_raw<T, BE>(pb) : load_part<T, BE>(pb, ok ? BE : 0);
+            rb = ok && a.vecb ? load_raw<T, BE>(pb) : load_part<T, BE>(pb, ok ? BE : 0);
             if (with_c) {
                 const T *pc = (const T *)a.Cm + (b.sp.r0 + t0 + bt) * a.ld_C + b.g * N + bk;
-                rc = ok && vecb ? load_raw<T, BE>(pc) : load_part<T, BE>(pc, ok ? BE : 0);
+                rc = ok && a.vecb ? load_raw<T, BE>(pc) : load_part<T, BE>(pc, ok ? BE : 0);
             }
         };
         auto put_bc = [&](bool with_c) {
@@ -534,7 +532,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) ssm_bwd_kernel(const SsmP a) {
                     }
                 }
                 const long long o = (b.sp.r0 + t0 + lt) * a.D + gc;
-                if ((a.vec & 2) && lleft >= EPT) {
+                if (a.vec_grad && lleft >= EPT) {
                     store_f32<T, EPT>((T *)a.du + o, du);
                     store_f32<T, EPT>((T *)a.ddt + o, dd);
                     if (a.z) store_f32<T, EPT>((T *)a.dz + o, dz);
@@ -652,10 +650,8 @@ cudaError_t run(const SsmArgs &a, cudaStream_t st) {
     using F = FwdShape<N>;
     static_assert(S::CH == 1024 / N, "bwd_parts");
     SsmP p = ssm_params<S::CH, S::EPT, S::BE>(a, kSpan);
-    // bit 0: inputs, bit 1: the gradients, whose rows are contiguous, as whole vectors
-    p.vec = (p.vec ? 1 : 0) | (p.Dg % S::EPT == 0 && a.D % S::EPT == 0 ? 2 : 0);
-    // bit 0: B and C for the main kernel, bit 1: for the sweep
-    p.vecb = (p.vecb ? 1 : 0) | (ssm_params<S::CH, S::EPT, F::BC>(a, kSpan).vecb ? 2 : 0);
+    p.vec_grad = p.Dg % S::EPT == 0;   // contiguous rows at 16 bytes
+    p.vecb_sweep = ssm_params<S::CH, S::EPT, F::BC>(a, kSpan).vecb;
     size_t off[6];
     bwd_parts(a, off);
     char *ws = (char *)a.workspace;

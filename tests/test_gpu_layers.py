@@ -449,6 +449,82 @@ def test_block_norm_of_zero_rows(K):
     assert x[0].isnan().all() and torch.isfinite(x[1]).all()
 
 
+# ------------------------------------------------------------------ rows at any element
+def _off(t, tail=1):
+    """The same rows one element into rows that are an odd number of elements longer."""
+    row = t.shape[-tail:].numel()
+    w = torch.full(t.shape[:-tail] + (row + 3,), NAN, dtype=t.dtype, device=t.device)
+    v = w[..., 1:1 + row].unflatten(-1, t.shape[-tail:])
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+@pytest.mark.parametrize("T", [1, 150])
+def test_ssm_rows_at_any_element(K, N, T, dtype):
+    """Widths of whole vectors in rows that start at none: each tensor alone, and all; the same bits as aligned rows."""
+    D, G = 256, 2
+    args, _, _, g = _ssm_inputs(_dense(2, T), D, N, G, True, True, True, True, 0, dtype)
+    u, dt, A, Bm, Cm, Ds, z, bias, h0 = args
+    dout, dhT = _n(g, 2, T, D, dtype=dtype), _n(g, 2, D, N)
+    rows = dict(u=(u, 1), dt=(dt, 1), Bm=(Bm, 2), Cm=(Cm, 2), z=(z, 1), dout=(dout, 1))
+
+    def run(off):
+        r = {k: _off(t, n) if k in off else t.contiguous() for k, (t, n) in rows.items()}
+        a = (r["u"], r["dt"], A, r["Bm"], r["Cm"], Ds, r["z"], bias)
+        step = tuple(t[:, 0] if t is not None and t.dim() > 2 else t for t in a)
+        h = h0.clone()
+        o = _off(u) if "u" in off else torch.empty_like(u)
+        out, hT = K.ssm_scan_fwd(*a, h0, out=o)
+        return (out, hT, *K.ssm_scan_bwd(*a, h0, r["dout"], dhT), K.ssm_step(*step, h), h)
+
+    want = run(())
+    for off in [(k,) for k in rows] + [("Bm", "Cm"), tuple(rows)]:
+        for i, (a, b) in enumerate(zip(run(off), want)):
+            assert torch.equal(a, b), (off, i)
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_conv_rows_at_any_element(K, dtype):
+    x, w, b, s0, _, _, g = _conv_inputs(_dense(2, 70), 64, 4, True, True, dtype, 0)
+    dy, dsT = _n(g, *x.shape, dtype=dtype), _n(g, 2, 3, 64)
+
+    def run(x, dy, y):
+        st = s0.clone()
+        y, sT = K.short_conv_fwd(x, w, b, s0, y=y)
+        return (y, sT, *K.short_conv_bwd(x, w, b, s0, dy, dsT), K.short_conv_step(x[:, 0], w, b, st), st)
+
+    want = run(x, dy, torch.empty_like(x))
+    for a, b_, y in ((_off(x), dy, torch.empty_like(x)), (x, _off(dy), torch.empty_like(x)), (x, dy, _off(x)),
+                     (_off(x), _off(dy), _off(x))):
+        for i, (o, r) in enumerate(zip(run(a, b_, y), want)):
+            assert torch.equal(o, r), i
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("D", [64, 2048, 4096])
+def test_norm_rows_at_any_element(K, D, dtype):
+    """Each row tensor alone, and all: against the 64-bit form (the order of a row's sum depends on the vectors)."""
+    g = _gen(D)
+    r, b, gate, dres, dx = (_n(g, 5, D, dtype=dtype) for _ in range(5))
+    s, wp, wx = (_u(g, 0.3, 1.5, D) for _ in range(3))
+    n, eps = 16 + 10 + 48, 1e-5
+    ref = (R.d(r), R.d(b), R.d(gate), R.d(s), R.d(wp), R.d(wx))
+    rr, rx = R.norm_fwd(*ref, eps)
+    far = ref[0].abs() + (rr - ref[0]).abs()
+    args = (*ref, R.d(dres), R.d(dx), eps)   # r stands for the stored sum here
+    want, mag = R.norm_bwd(*args), R.norm_bwd(*args, mag=True)
+    for off in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 1)):
+        t = [_off(v) if o else v for v, o in zip((r, b, gate), off)]
+        res, x = K.block_norm_fwd(*t, s, wp, wx, eps=eps)
+        R.check("res_out", res, rr, far, n)
+        R.check("x", x, rx, far * (rx / rr).abs().nan_to_num() + rx.abs(), n)
+        for name, o, w, f in zip(("dresidual", "dblock", "dgate", "dscale", "dw_post", "dw_pre"),
+                                 K.block_norm_bwd(*t, s, wp, wx, dres, dx, eps=eps), want, mag):
+            R.check(name, o, w, f, 2 * n + (5 if o.dim() == 1 else 0))
+
+
 # ------------------------------------------------------------------ how they are called
 def _calls(K, seed=0, dtype=torch.bfloat16):
     """One call of each operator, as (name, function of nothing, outputs)."""
