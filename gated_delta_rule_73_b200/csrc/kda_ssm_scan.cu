@@ -14,11 +14,13 @@
 //    the special-function unit's rate.
 //  * whole sequences, four states a lane (ssm_seq_kernel): four times the lanes, and warps of their
 //    own for what surrounds the recurrence, so that a few thousand channels fill the device without
-//    a second pass over the exponentials: 302 us for 8192 x 4096 x 16, where the first takes 1780.
+//    a second pass over the exponentials: 306 us for 8192 x 4096 x 16, where the first takes 1780.
 //  * spans of time side by side (ssm_fwd_kernel twice): a span's effect on the state is
 //    h -> exp(A sum delta) h + (its end from zero), so one sweep finds the ends of all spans, a small
 //    pass chains them, and the spans then run side by side, for twice the exponentials: 82 us for
 //    8192 x 256 x 16, where whole sequences take 301 at best.
+#include <type_traits>
+
 #include "kda_ssm.cuh"
 
 namespace kda {
@@ -216,15 +218,44 @@ struct SeqShape {
     };
 };
 
-template <typename T, int N>
+// The sequence that is the rank-th longest of up to 32, whole: blocks start in the order of their
+// numbers, and a long sequence that starts last is what all others then wait for.  8192 x 1024 x 16 in
+// 20 random sequences: 81 us against 107 in the order given; 3001 x 1002 x 32 in 7: 54 to 62 against 64
+// to 74.  Not where a sequence's blocks alone would share SMs by twos while others run (8100 x 4096 x
+// 16, all but 100 rows one sequence: 515 us where it comes first, 303 where it comes last), nor for
+// short ones, which the ranking would hold up (64 x 2048 x 16 in 32: 51 against 39).
+__device__ __forceinline__ Span longest_first(const Seqs &q, int rank) {
+    const int lane = threadIdx.x & 31;
+    const int len = lane < q.S ? (int)(q.hi(lane) - q.lo(lane)) : -1;
+    int before = 0;
+    for (int j = 0; j < q.S; ++j) {
+        const int other = __shfl_sync(0xffffffffu, len, j);
+        before += other > len || (other == len && j < lane);
+    }
+    Span x = {};
+    x.seq = __reduce_max_sync(0xffffffffu, lane < q.S && before == rank ? lane : -1);
+    x.count = 1;
+    if (x.seq >= 0) {
+        x.r0 = q.lo(x.seq);
+        x.n = (int)(q.hi(x.seq) - x.r0);
+    }
+    return x;
+}
+
+template <typename T, int N, bool RANKED>
 __global__ void __launch_bounds__(SeqShape<T, N>::THREADS, 2) ssm_seq_kernel(const SsmP a) {
     using S = SeqShape<T, N>;
     constexpr int SPT = S::SPT, NL = S::NL, CH = S::CH, TT = S::TT, EV = S::EV, PASS = S::PASS, TPR = S::TPR, TSTEP = S::TSTEP, VB = S::VB,
                   BPT = S::BPT, ST = S::STAGES, ALL = S::THREADS;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     typename S::Stage *stage = reinterpret_cast<typename S::Stage *>(smem_raw);
-    const SsmBlock b = ssm_block(a, CH);
+    SsmBlock b = ssm_block(a, CH);
+    if (RANKED) b.sp = longest_first(a.q, (int)b.slot);
     if (b.sp.seq < 0) return;
+    // rows are fewer than 2^31; out of the ranking they take registers of every thread, of which none are left
+    using Row = typename std::conditional<RANKED, int, long long>::type;
+    const Row r0 = (Row)b.sp.r0;
+    const int seq = b.sp.seq;
     const int n = b.sp.n, tiles = (n + TT - 1) / TT;
     const int FULL = 1, DONE = 1 + ST;
     if (threadIdx.x < S::SCAN) {
@@ -234,7 +265,7 @@ __global__ void __launch_bounds__(SeqShape<T, N>::THREADS, 2) ssm_seq_kernel(con
         const int at_y = spread(tid >> 2) * 4 + (tid & 3);
         float A2[SPT], h[SPT];
         load_f32<float, SPT>(a.A + c * N + q * SPT, A2);
-        const float *src = a.h0 ? a.h0 + ((long long)b.sp.seq * a.D + c) * N : nullptr;
+        const float *src = a.h0 ? a.h0 + ((long long)seq * a.D + c) * N : nullptr;
 #pragma unroll
         for (int i = 0; i < SPT; ++i) {
             A2[i] = rate(A2[i]);
@@ -290,7 +321,7 @@ __global__ void __launch_bounds__(SeqShape<T, N>::THREADS, 2) ssm_seq_kernel(con
             arrive_at<ALL>(DONE + i % ST);
         }
         if (!live) return;
-        if (a.h_T) store_f32<float, SPT>(a.h_T + ((long long)b.sp.seq * a.D + c) * N + q * SPT, h);
+        if (a.h_T) store_f32<float, SPT>(a.h_T + ((long long)seq * a.D + c) * N + q * SPT, h);
         return;
     }
     // helpers
@@ -307,8 +338,8 @@ __global__ void __launch_bounds__(SeqShape<T, N>::THREADS, 2) ssm_seq_kernel(con
     }
     const int bt = tid / BPT, bk = tid % BPT * VB;
     const bool is_b = bk < N;
-    const T *pbc = is_b ? (const T *)a.Bm + (b.sp.r0 + bt) * a.ld_B + b.g * N + bk
-                        : (const T *)a.Cm + (b.sp.r0 + bt) * a.ld_C + b.g * N + bk - N;
+    const T *pbc = is_b ? (const T *)a.Bm + (long long)(r0 + bt) * a.ld_B + b.g * N + bk
+                        : (const T *)a.Cm + (long long)(r0 + bt) * a.ld_C + b.g * N + bk - N;
     const long long ldbc = is_b ? a.ld_B : a.ld_C;
     constexpr int DEPTH = 2;   // a tile's loads are two tiles on the way: a tile takes a microsecond, HBM's latency is more
     struct Next {
@@ -320,9 +351,9 @@ __global__ void __launch_bounds__(SeqShape<T, N>::THREADS, 2) ssm_seq_kernel(con
         for (int p = 0; p < PASS; ++p) {
             const int t = t0 + p * TSTEP + lt;
             const bool ok = t < n && p * TSTEP + lt < TT;
-            x.u[p] = load_tile<T, EV>(a.u, b.sp.r0 + t, a.ld_u, c, left, ok, a.vec);
-            x.d[p] = load_tile<T, EV>(a.dt, b.sp.r0 + t, a.ld_dt, c, left, ok, a.vec);
-            if (gate) x.z[p] = load_tile<T, EV>(a.z, b.sp.r0 + t, a.ld_z, c, left, ok, a.vec);
+            x.u[p] = load_tile<T, EV>(a.u, r0 + t, a.ld_u, c, left, ok, a.vec);
+            x.d[p] = load_tile<T, EV>(a.dt, r0 + t, a.ld_dt, c, left, ok, a.vec);
+            if (gate) x.z[p] = load_tile<T, EV>(a.z, r0 + t, a.ld_z, c, left, ok, a.vec);
         }
         const bool ok = t0 + bt < n;
         x.bc = ok && a.vecb ? load_raw<T, VB>(pbc + t0 * ldbc) : load_part<T, VB>(pbc + t0 * ldbc, ok ? VB : 0);
@@ -380,7 +411,7 @@ __global__ void __launch_bounds__(SeqShape<T, N>::THREADS, 2) ssm_seq_kernel(con
                     y[k] = fmaf(skip[k], u[k], part[k * NL]);
                     if (gate) y[k] *= silu_f32(z[k]);
                 }
-                T *o = (T *)a.out + (b.sp.r0 + t0 + t) * a.ld_out + c;
+                T *o = (T *)a.out + (long long)(r0 + t0 + t) * a.ld_out + c;
                 if (a.vec && left >= EV) store_f32<T, EV>(o, y);
                 else store_part<T, EV>(o, y, left);
             }
@@ -524,8 +555,11 @@ __global__ void __launch_bounds__(128) ssm_step_kernel(const SsmP a, int per) {
 //   four states a lane   a token 38 with one block a SM, 65 with two, and so on in pairs
 //   a lane a channel     a token 100 + 105 k, k warps a scheduler (at least one), from four on 68 + 113 k
 //   spans                0.00076 an update and 0.0024 a channel and token, and 20 us for its passes
-// Packed sequences' lengths are not known here: they count as 1.5 times the mean, and a span
-// holds twice the mean of as many rows as spans are wanted, so that even sequences stay whole.
+// Packed sequences' lengths are not known here.  The longest counts as 1.5 times the mean for four states
+// a lane, whose blocks queue and share the SMs evenly, and as twice the mean for a lane a channel,
+// whose blocks run at once and wait for the longest (8192 x 4096 x 16 in 20 random sequences: 257
+// to 277 us against 306 to 499; 64 x 2048 x 16 in 32 sequences: 39 against 8).  A span holds twice
+// the mean of as many rows as spans are wanted, so that even sequences stay whole.
 struct FwdPlan {
     bool lanes;   // four states a lane
     int L;
@@ -533,12 +567,18 @@ struct FwdPlan {
 FwdPlan plan(const SsmArgs &a) {
     const int Dg = a.D / a.G, ch_seq = 512 / a.N, ch = kFwdThreads / (a.N <= 16 ? 1 : a.N / 16);
     const long long rows = a.rows, whole = a.T > 0 ? a.T : 1;
-    const double len = a.cu && a.S > 1 ? 1.5 * rows / a.S : (double)a.T;
     const long long blocks_seq = (long long)a.S * a.G * ((Dg + ch_seq - 1) / ch_seq), per_span = (long long)a.G * ((Dg + ch - 1) / ch);
-    const long long n = (blocks_seq + 147) / 148;
-    const double t_seq = len * (n / 2 * 65.0 + n % 2 * 38.0);
     const double k = (double)per_span * a.S / 148.0;   // warps a scheduler: blocks of four warps
-    const double t_whole = len * (k <= 4.0 ? 100.0 + 105.0 * (k > 1.0 ? k : 1.0) : 68.0 + 113.0 * k);
+    double t_seq, t_whole;
+    if (a.cu && a.S > 1) {
+        const double mean = (double)rows / a.S, some = 100.0 + 105.0 * (k > 4.0 ? 4.0 : k > 1.0 ? k : 1.0);
+        t_seq = fmax(1.5 * mean * (blocks_seq > 148 ? 65.0 : 38.0), blocks_seq / 148.0 * (mean * 36.0 + 3000.0));
+        t_whole = fmax(2.0 * mean * some, mean * (68.0 + 113.0 * k));
+    } else {
+        const long long n = (blocks_seq + 147) / 148;
+        t_seq = a.T * (n / 2 * 65.0 + n % 2 * 38.0);
+        t_whole = a.T * (k <= 4.0 ? 100.0 + 105.0 * (k > 1.0 ? k : 1.0) : 68.0 + 113.0 * k);
+    }
     const double t_span = (double)rows * a.D * (0.00076 * a.N + 0.0024) + 20000.0;
     if (t_span < t_seq && t_span < t_whole) {
         const long long want = 592 / per_span > 1 ? 592 / per_span : 1;   // spans in all: one wave of 4 blocks a SM
@@ -558,10 +598,13 @@ cudaError_t run_seq(const SsmArgs &a, cudaStream_t st) {
     const long long blocks = p.slots * p.nblk;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     constexpr int smem = sizeof(typename S::Stage) * S::STAGES;
-    const cudaError_t e = cudaFuncSetAttribute(ssm_seq_kernel<T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // see longest_first
+    const bool ranked = a.cu && a.S <= 32 && a.T >= 128LL * a.S && p.nblk <= 74;
+    const auto kernel = ranked ? ssm_seq_kernel<T, N, true> : ssm_seq_kernel<T, N, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     a.marks->mark(st);
-    ssm_seq_kernel<T, N><<<(unsigned)blocks, S::THREADS, smem, st>>>(p);
+    kernel<<<(unsigned)blocks, S::THREADS, smem, st>>>(p);
     return cudaGetLastError();
 }
 

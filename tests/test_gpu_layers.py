@@ -449,6 +449,38 @@ def test_block_norm_of_zero_rows(K):
     assert x[0].isnan().all() and torch.isfinite(x[1]).all()
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+def test_ssm_order_of_sequences(K, N, dtype):
+    """Long sequences start first; each has the values that it has alone, equal lengths and empty ones too."""
+    D = 40
+    for lens in ([300, 0, 700, 128, 300, 1], [10] + 31 * [140], [0, 0, 900]):
+        cuts = [7]
+        for n in lens:
+            cuts.append(cuts[-1] + n)
+        args, cu, bounds, _ = _ssm_inputs(_packed(cuts, cuts[-1] + 4), D, N, 2, True, True, True, True, 0, dtype)
+        u, dt, A, Bm, Cm, Ds, z, bias, h0 = args
+        out, hT = K.ssm_scan_fwd(*args, cu_seqlens=cu)
+        assert (out[:7] == 0).all() and (out[-4:] == 0).all()
+        ro, rh = _ssm_ref(args, bounds)
+        fo, fh = _ssm_ref(args, bounds, mag=True)
+        R.check("out", out[7:-4], ro[7:-4], fo[7:-4], 24 * max(lens) + N + 64)
+        R.check("h_T", hT, rh, fh, 24 * max(lens) + 64)
+
+
+def test_bounds_outside_the_rows_are_cut_off(K):
+    for D, T in ((24, 100), (8, 1500)):   # whole sequences, spans of time
+        at = _packed([0, 3, 70, T], T)
+        x, w, b, s0, cu, _, g = _conv_inputs(at, D, 4, True, True, torch.float32, 0)
+        a, _, _, _ = _ssm_inputs(at, D, 8, 1, True, True, True, True, 0, torch.float32)
+        dy, dsT, dh = _n(g, T, D), _n(g, 3, 3, D), _n(g, 3, D, 8)
+        run = lambda cu: (*K.short_conv_fwd(x, w, b, s0, cu_seqlens=cu),  # noqa: E731
+                          *K.short_conv_bwd(x, w, b, s0, dy, dsT, cu_seqlens=cu),
+                          *K.ssm_scan_fwd(*a, cu_seqlens=cu), *K.ssm_scan_bwd(*a, dy, dh, cu_seqlens=cu))
+        far = torch.tensor([-5, 3, 70, T + 1000], dtype=torch.int32, device="cuda")
+        assert all(torch.equal(p, q) for p, q in zip(run(far), run(cu)))
+
+
 # ------------------------------------------------------------------ rows at any element
 def _off(t, tail=1):
     """The same rows one element into rows that are an odd number of elements longer."""
