@@ -9,7 +9,7 @@
 // and walks L rows with the K-1 rows before them in registers, so a row is read once by its own walk
 // and K-1 times more, from L2, at the seams.  Neighbouring threads hold neighbouring channels: rows
 // are read in whole sectors.  Pairs go through packed FP32 instructions, which halves the issue slots.  bf16, K = 4: forward 8192 x 12288 in 74 us (5.4 TB/s), backward 16384 x
-// 2048 in 70 us (2.9 TB/s: 96 registers leave 18 warps an SM to cover HBM's latency), step 256 x 12288
+// 2048 in 70 us (2.9 TB/s; 69 instructions a pair of channels and row), step 256 x 12288
 // in 8.2 us (6.2 TB/s).
 #include "kda_layers_internal.h"
 #include "kda_rows.cuh"
