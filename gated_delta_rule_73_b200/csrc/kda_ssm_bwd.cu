@@ -6,7 +6,7 @@
 //   ddelta_t = sum_n e_t a_t h_{t-1} A + u_t sum_n e_t B_t,   du_t = Dskip dy_t + delta_t sum_n e_t B_t
 //   dz_t = dout_t y_t silu'(z_t),   ddt = ddelta sigmoid(dt + dt_bias),   dh0 = a_1 e_1
 //
-// Time is cut into spans of 64 tokens that run side by side.  One sweep finds for every span its
+// Time is cut into spans of up to 64 tokens that run side by side.  One sweep finds for every span its
 // end state from zero and, with the running product P of the a, the gradient at its start that
 // its own outputs make, sum_t P_t C_t dy_t: both go forward, on the same exponentials.  A small
 // pass chains the spans.  The main kernel then walks its span forward once, keeping the state
@@ -21,7 +21,7 @@
 namespace kda {
 namespace {
 
-constexpr int kSpan = 64;      // tokens a span
+constexpr int kSpan = 64;      // tokens a span, at most
 
 // Both sweeps of a span: end state from zero (hst), gradient at the start (gst), sum of delta.
 // Lanes and loads as in the forward's ssm_fwd_kernel: a lane a channel, 16 states.
@@ -630,11 +630,33 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 long long part_ld(const SsmArgs &a) { return ((long long)a.D * (a.N + 2) + 3) / 4 * 4; }
 
+// Rows a span takes: the main kernel's time goes by the waves of 444 blocks (three an SM) and by a
+// span's rows in each, with 24 rows' worth for a block's start and end; the chain through a
+// sequence's spans takes a quarter of a row's time for each.  Few blocks take short spans, many
+// stay at 64: 4 x 256 x 512 x 8 takes 43 us with 16 rows a span and 94 with 64, 512 x 1024 x 16 46 with 32 rows
+// and 62 with 64, 2 x 900 x 900 x 8 106 with 40 and 131 with 64.  Larger calls keep 64: 8192 x 1024 x 32 takes 567 us
+// with 64 and 577 with 56.
+int span_rows(const SsmArgs &a) {
+    const int CH = 1024 / a.N, Dg = a.D / a.G;
+    const long long nblk = (long long)a.G * ((Dg + CH - 1) / CH);
+    int best = kSpan;
+    double least = 0.0;
+    for (int L = kSpan; L >= 2 * kStep; L -= kStep) {
+        const long long waves = (span_slots(a.cu != nullptr, a.S, a.T, L) * nblk + 443) / 444;
+        const double cost = (double)waves * (L + 24) + 0.25 * (double)(a.T / L);
+        if (L == kSpan || cost < least) {
+            least = cost;
+            best = L;
+        }
+    }
+    return best;
+}
+
 // Parts of the workspace: hst, gst, sdel, part, part_BC; off[5] is the whole.
 void bwd_parts(const SsmArgs &a, size_t (&off)[6]) {
     const int CH = 1024 / a.N, Dg = a.D / a.G;
     const size_t nblk = (size_t)a.G * ((Dg + CH - 1) / CH);
-    const size_t slots = (size_t)span_slots(a.cu != nullptr, a.S, a.T, kSpan);
+    const size_t slots = (size_t)span_slots(a.cu != nullptr, a.S, a.T, span_rows(a));
     const size_t sd = slots * a.D * sizeof(float);
     off[0] = 0;
     off[1] = off[0] + up256(sd * a.N);
@@ -649,9 +671,10 @@ cudaError_t run(const SsmArgs &a, cudaStream_t st) {
     using S = BwdShape<T, N>;
     using F = FwdShape<N>;
     static_assert(S::CH == 1024 / N, "bwd_parts");
-    SsmP p = ssm_params<S::CH, S::EPT, S::BE>(a, kSpan);
+    const int L = span_rows(a);
+    SsmP p = ssm_params<S::CH, S::EPT, S::BE>(a, L);
     p.vec_grad = p.Dg % S::EPT == 0;   // contiguous rows at 16 bytes
-    p.vecb_sweep = ssm_params<S::CH, S::EPT, F::BC>(a, kSpan).vecb;
+    p.vecb_sweep = ssm_params<S::CH, S::EPT, F::BC>(a, L).vecb;
     size_t off[6];
     bwd_parts(a, off);
     char *ws = (char *)a.workspace;

@@ -181,6 +181,7 @@ SSM = [
     (_dense(250, 2), 384, 16, 1, True, True, True, True, 0),
     (_dense(250, 2), 93, 64, 1, False, True, True, True, 0),
     (_dense(300, 3), 162, 32, 3, True, False, False, True, 0),
+    (_dense(12, 126), 4096, 16, 1, True, True, True, True, 0),   # enough blocks for the longest spans of the backward
     (_packed(sorted([0] + [(i * 7919) % 601 for i in range(260)] + [601]), 601), 380, 16, 1, True, True, True, True, 4),
 ] if torch.cuda.is_available() else []
 
