@@ -379,6 +379,12 @@ NORM = [
     ((1300,), 1032, True, True, True, 0),
     ((4000,), 40, True, True, True, 0),
     ((4,), 256, False, False, True, 0),
+    ((200,), 1002, True, True, True, 0),
+    ((200,), 4100, True, True, True, 0),
+    ((160,), 5001, True, True, True, 0),
+    ((160,), 6002, True, False, False, 0),
+    ((160,), 8200, False, False, True, 0),
+    ((301,), 11002, True, True, True, 0),
     ((0,), 256, True, True, True, 0),
 ] if torch.cuda.is_available() else []
 
