@@ -498,8 +498,11 @@ cudaError_t launch(const NormArgs &a, bool bwd, cudaStream_t st) {
         if (n > 0) block_norm_bwd_kernel<T, V, E, NT><<<n, nt, 0, st>>>(p);
     } else {
         const int smem = 2 * V * E * nt * (int)sizeof(float);
+        // The limit is kept per kernel for all host threads: every call sets the same one, that of 1024
+        // threads, and a call of fewer cannot take it away from another's launch.
+        constexpr int most = 2 * V * E * 1024 * (int)sizeof(float);
         const cudaError_t e = cudaFuncSetAttribute(block_norm_bwd_wide_kernel<T, V, E>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
         if (n > 0) block_norm_bwd_wide_kernel<T, V, E><<<n, nt, smem, st>>>(p);
     }

@@ -7,6 +7,8 @@ hardware's exponential and reciprocal are off by 2 half-steps or so each, and an
 argument x also by 1.5 |x| half-steps for the argument's own rounding, |x| < 20 here).  For the
 recursion each token adds the same again, at most 24: its decay factor's, delta's, the products'.
 """
+import threading
+
 import pytest
 import torch
 
@@ -656,6 +658,44 @@ def test_offsets_beyond_31_bits(K):
     r, p = K.block_norm_fwd(x, u, z)
     r2, p2 = K.block_norm_fwd(x.contiguous(), u.contiguous(), z.contiguous())
     assert torch.equal(r, r2) and torch.equal(p, p2)
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_norm_backward_from_two_threads(K, dtype, monkeypatch):
+    """Two widths of one kernel, from two host threads through the C interface, which the interpreter's lock does
+    not order: neither thread may change what the other's launch was given."""
+    runs, jobs = 30000, []
+    for D in (8200, 16384):
+        g = _gen(D)
+        r, b, gate, dres, dx = (_n(g, 4, D, dtype=dtype) for _ in range(5))
+        s, wp, wx = (_u(g, 0.3, 1.5, D) for _ in range(3))
+        outs = [torch.empty_like(r) for _ in range(3)] + [torch.empty_like(s) for _ in range(3)]
+        ws = torch.empty(K.kda_block_norm_bwd_workspace_bytes(r), dtype=torch.uint8, device="cuda")
+        tensors = (r, b, gate, s, wp, wx, dres, dx, *outs, ws)
+        want = K.block_norm_bwd(*tensors[:8])
+        made = []
+        with monkeypatch.context() as m:
+            m.setattr(K.layers, "_launch", lambda fn, call, args, dims, opts, stream: made.append((fn, args, dims, opts)))
+            K.kda_block_norm_bwd(*tensors)
+        jobs.append((made[0], outs, want, torch.cuda.Stream(), tensors))
+    torch.cuda.synchronize()
+    ready, statuses = threading.Barrier(2), []
+
+    def work(call, stream):
+        fn, args, dims, opts = call
+        handle = stream.cuda_stream
+        ready.wait()
+        statuses.append({fn(*args, dims, opts, handle) for _ in range(runs)})
+
+    threads = [threading.Thread(target=work, args=(j[0], j[3])) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert statuses == [{0}, {0}]
+    for _, outs, want, _, _ in jobs:
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
 
 
 # ------------------------------------------------------------------ a run of them together
