@@ -152,23 +152,23 @@ struct Seqs {
     const int *cu;
     int S;
     long long T;
-    __device__ __forceinline__ long long rows() const { return cu ? T : T * S; }
-    __device__ __forceinline__ long long lo(int s) const {
+    __host__ __device__ __forceinline__ long long rows() const { return cu ? T : T * S; }
+    __host__ __device__ __forceinline__ long long lo(int s) const {
         if (!cu) return T * s;
         const long long v = cu[s];
         return v < 0 ? 0 : v > T ? T : v;
     }
-    __device__ __forceinline__ long long hi(int s) const {
+    __host__ __device__ __forceinline__ long long hi(int s) const {
         if (!cu) return T * (s + 1);
         const long long a = lo(s), b = lo(s + 1);
         return b < a ? a : b;
     }
     // the last sequence that starts at or before row r (0 if none does)
-    __device__ __forceinline__ int at(long long r) const {
+    __host__ __device__ __forceinline__ int at(long long r) const {
         if (!cu) return T > 0 ? (int)(r / T) : 0;
         int a = 0, b = S;   // lo(a) <= r (or a == 0), lo(b) > r (or b == S)
         while (b - a > 1) {
-            const int m = (a + b) >> 1;
+            const int m = a + ((b - a) >> 1);   // a + b may not fit an int
             if (lo(m) <= r) a = m; else b = m;
         }
         return a;
@@ -190,12 +190,12 @@ __host__ __device__ __forceinline__ long long span_slots(bool packed, int S, lon
     const long long per = (T + L - 1) / L;
     return (per > 0 ? per : 1) * S;
 }
-__device__ __forceinline__ long long first_slot(const Seqs &q, int s, long long L) {
+__host__ __device__ __forceinline__ long long first_slot(const Seqs &q, int s, long long L) {
     if (q.cu) return q.lo(s) / L + s;
     const long long per = (q.T + L - 1) / L;
     return (per > 0 ? per : 1) * s;
 }
-__device__ __forceinline__ Span span_at(const Seqs &q, long long slot, long long L) {
+__host__ __device__ __forceinline__ Span span_at(const Seqs &q, long long slot, long long L) {
     Span x;
     int s;
     if (!q.cu) {
@@ -204,7 +204,7 @@ __device__ __forceinline__ Span span_at(const Seqs &q, long long slot, long long
     } else {
         int a = 0, b = q.S;
         while (b - a > 1) {
-            const int m = (a + b) >> 1;
+            const int m = a + ((b - a) >> 1);   // a + b may not fit an int
             if (q.lo(m) / L + m <= slot) a = m; else b = m;
         }
         s = a;

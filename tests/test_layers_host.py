@@ -1,5 +1,7 @@
 """Refusals of the operators of kda_layers.h: on the host, before any CUDA call (no GPU needed)."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
@@ -204,3 +206,33 @@ def test_workspace_sizes(L):
     n = L._lib.kda_block_norm_bwd_workspace_bytes
     assert n(_norm(L), None) == 4 * 2 * 64 * 4 and n(_norm(L, rows=1 << 20), None) < 1 << 24
     assert ctypes.sizeof(L.kda_conv_dims) == 64 and ctypes.sizeof(L.kda_ssm_dims) == 88
+
+
+# ------------------------------------------------------------------ index arithmetic that kernels and launchers share
+def _host_program(tmp_path, body, header="kda_rows.cuh"):
+    """Compiles `body` against a header of the kernels and runs it on the CPU; its output."""
+    from gated_delta_rule_73_b200 import build as B
+    src, exe = tmp_path / "p.cu", str(tmp_path / "p")
+    src.write_text(f'#include <stdio.h>\n#include <stdlib.h>\n#include "{header}"\n'
+                   f"using namespace kda;\nint main() {{\n{body}\nreturn 0;\n}}\n")
+    subprocess.run([B._nvcc(), "-O1", "-std=c++17", *B.ARCH, "-I" + B.INC, "-I" + B.CSRC, str(src), "-o", exe], check=True,
+                   capture_output=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120, cwd=os.fspath(tmp_path))
+    assert r.returncode == 0, (r.returncode, r.stderr)
+    return r.stdout.split()
+
+
+def test_sequence_search_in_the_largest_tables(tmp_path):
+    """Packed calls may have up to 2^31 - 1 sequences, nearly all of them empty: the search for a row's sequence
+    and for a slot's reads inside the table at every size."""
+    out = _host_program(tmp_path, """
+    for (long long S : {3LL, (1LL << 30) + 5, (1LL << 31) - 1}) {
+        int *cu = (int *)calloc(S + 1, sizeof(int));   // bounds of empty sequences; the pages stay untouched
+        if (!cu) return 1;
+        cu[S] = 100;
+        const Seqs q{cu, (int)S, 100};
+        const Span x = span_at(q, S - 1, 64), y = span_at(q, S, 64);   // 64 and 36 rows of the last sequence
+        printf("%d %d %d %d %d %d %d\\n", q.at(0) == S - 1, q.at(99) == S - 1, x.seq == S - 1, (int)x.r0, x.n, (int)y.r0, y.n);
+        free(cu);
+    }""")
+    assert out == 3 * ["1", "1", "1", "0", "64", "64", "36"]
