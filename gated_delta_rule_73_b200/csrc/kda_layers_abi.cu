@@ -197,7 +197,7 @@ int kda_short_conv_fwd(const void *x, const void *w, const void *bias, const voi
     const long long es = a.bf16 ? 2 : 4, ns = (long long)a.S * (a.K - 1) * a.D, D = a.D;
     if (!distinct({rows_of(y, a.rows, a.ld_y, D, a.bf16), flat(state_T, ns * es)},
                   {rows_of(x, a.rows, a.ld_x, D, a.bf16), flat(w, D * a.K * es), flat(bias, D * es), flat(state0, ns * es),
-                   flat(a.cu, a.cu ? 4LL * (a.S + 1) : 0)}))
+                   flat(a.cu, a.cu ? 4 * (a.S + 1LL) : 0)}))
         return KDA_ERR_ARG;
     a.x = x; a.w = w; a.bias = bias; a.state0 = state0; a.y = y; a.state_T = state_T;
     LaunchMarks m = marks_of(o);
@@ -229,7 +229,7 @@ int kda_short_conv_bwd(const void *x, const void *w, const void *bias, const voi
     if (!distinct({rows_of(dx, a.rows, a.ld_dx, D, a.bf16), flat(dw, D * a.K * 4), flat(dbias, D * 4), flat(dstate0, ns * 4),
                    flat(o.workspace, (long long)need)},
                   {rows_of(x, a.rows, a.ld_x, D, a.bf16), flat(w, D * a.K * es), flat(bias, D * es), flat(state0, ns * es),
-                   rows_of(dy, a.rows, a.ld_y, D, a.bf16), flat(dstate_T, ns * 4), flat(a.cu, a.cu ? 4LL * (a.S + 1) : 0)}))
+                   rows_of(dy, a.rows, a.ld_y, D, a.bf16), flat(dstate_T, ns * 4), flat(a.cu, a.cu ? 4 * (a.S + 1LL) : 0)}))
         return KDA_ERR_ARG;
     if (need > 0 && (!o.workspace || o.workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     a.x = x; a.w = w; a.bias = bias; a.state0 = state0; a.dy = dy; a.dstate_T = dstate_T;
@@ -306,7 +306,7 @@ int kda_ssm_scan_fwd(const void *u, const void *dt, const float *A, const void *
     if (!distinct({rows_of(out, a.rows, a.ld_out, D, a.bf16), flat(h_T, ns), flat(o.workspace, (long long)need)},
                   {rows_of(u, a.rows, a.ld_u, D, a.bf16), rows_of(dt, a.rows, a.ld_dt, D, a.bf16), rows_of(z, a.rows, a.ld_z, D, a.bf16),
                    rows_of(Bm, a.rows, a.ld_B, bc, a.bf16), rows_of(Cm, a.rows, a.ld_C, bc, a.bf16), flat(A, D * a.N * 4),
-                   flat(Dskip, D * 4), flat(dt_bias, D * 4), flat(h0, ns), flat(a.cu, a.cu ? 4LL * (a.S + 1) : 0)}))
+                   flat(Dskip, D * 4), flat(dt_bias, D * 4), flat(h0, ns), flat(a.cu, a.cu ? 4 * (a.S + 1LL) : 0)}))
         return KDA_ERR_ARG;
     if (need > 0 && (!o.workspace || o.workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     a.u = u; a.dt = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.Dskip = Dskip; a.z = z; a.dt_bias = dt_bias;
@@ -346,7 +346,7 @@ int kda_ssm_scan_bwd(const void *u, const void *dt, const float *A, const void *
                   {rows_of(u, a.rows, a.ld_u, D, a.bf16), rows_of(dt, a.rows, a.ld_dt, D, a.bf16), rows_of(z, a.rows, a.ld_z, D, a.bf16),
                    rows_of(Bm, a.rows, a.ld_B, bc, a.bf16), rows_of(Cm, a.rows, a.ld_C, bc, a.bf16), flat(A, D * a.N * 4),
                    flat(Dskip, D * 4), flat(dt_bias, D * 4), flat(h0, ns),
-                   rows_of(dout, a.rows, a.ld_out, D, a.bf16), flat(dh_T, ns), flat(a.cu, a.cu ? 4LL * (a.S + 1) : 0)}))
+                   rows_of(dout, a.rows, a.ld_out, D, a.bf16), flat(dh_T, ns), flat(a.cu, a.cu ? 4 * (a.S + 1LL) : 0)}))
         return KDA_ERR_ARG;
     if (need > 0 && (!o.workspace || o.workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     a.u = u; a.dt = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.Dskip = Dskip; a.z = z; a.dt_bias = dt_bias;

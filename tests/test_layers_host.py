@@ -144,6 +144,19 @@ def test_norm_refusals(L):
     assert bwd(_norm(L), same=[(8, 7)], opts=ok) == ARG and bwd(_norm(L), same=[(9, 6)], opts=ok) == ARG
 
 
+@host_only
+def test_outputs_over_the_largest_table_of_bounds(L):
+    """The table of 2^31 - 1 sequences is 8 GB long, to the call's check of what its outputs overlap as well."""
+    n, at = (1 << 31) - 1, 1 << 36
+    inside = at + (1 << 32)
+    for name, pointers, d, out, ok in (
+            ("kda_short_conv_fwd", 6, _conv(L, B=n, T=4, cu_seqlens=at), 4, (2, 3, 5)),
+            ("kda_short_conv_bwd", 10, _conv(L, B=n, T=4, cu_seqlens=at), 6, (2, 3, 5, 8, 9)),
+            ("kda_ssm_scan_fwd", 11, _ssm(L, B=n, T=4, D=2, N=8, cu_seqlens=at), 9, (5, 6, 7, 8, 10)),
+            ("kda_ssm_scan_bwd", 20, _ssm(L, B=n, T=4, D=2, N=8, cu_seqlens=at), 11, (5, 7, 8, 10, 16, 18, 19))):
+        assert _call(L, name, pointers, d, null=ok, at=[(out, inside)], opts=_opts(L, 1 << 50, 1 << 62)) == ARG, name
+
+
 def test_binding_refuses_what_the_library_could_not_see(L):
     x, w = torch.zeros(1, 4, 8), torch.zeros(8, 4)
     with pytest.raises(ValueError, match="CUDA"):
