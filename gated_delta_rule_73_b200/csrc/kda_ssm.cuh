@@ -149,6 +149,18 @@ SsmP ssm_params(const SsmArgs &a, int L) {
     return p;
 }
 
+// One token: the sequences in `count` parts of `per`, for 2368 blocks with `blocks` of channels.
+struct StepParts {
+    int per, count;
+};
+inline StepParts step_parts(int S, int blocks) {
+    const int parts = 2368 / blocks > 1 ? 2368 / blocks : 1;
+    StepParts x;
+    x.per = (int)(((long long)S + parts - 1) / parts);
+    x.count = (int)(((long long)S + x.per - 1) / x.per);
+    return x;
+}
+
 // Start states of the spans (hst) from the spans' own ends, and, where gst is set, the
 // gradients at the spans' ends from the spans' own gradients at their starts.
 cudaError_t launch_ssm_seams(const SsmP &p, int N, cudaStream_t st);

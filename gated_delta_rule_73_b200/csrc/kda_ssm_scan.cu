@@ -636,13 +636,13 @@ template <typename T, int N>
 cudaError_t run_step(const SsmArgs &a, cudaStream_t st) {
     const SsmP p = ssm_params<1, 1, 4>(a, 1);
     constexpr int R = N == 8 ? 2 : 4;
-    const int blocks = (a.D + 512 / N - 1) / (512 / N), parts = 2368 / blocks > 1 ? 2368 / blocks : 1;
-    const int per = (a.S + parts - 1) / parts, n = (a.S + per - 1) / per;
-    if (n > 65535) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)blocks, (unsigned)n);
+    const int blocks = (a.D + 512 / N - 1) / (512 / N);
+    const StepParts x = step_parts(a.S, blocks);
+    if (x.count > 65535) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)blocks, (unsigned)x.count);
     a.marks->mark(st);
-    if (per >= R) ssm_step_kernel<T, N, R><<<grid, 128, 0, st>>>(p, per);
-    else ssm_step_kernel<T, N, 1><<<grid, 128, 0, st>>>(p, per);
+    if (x.per >= R) ssm_step_kernel<T, N, R><<<grid, 128, 0, st>>>(p, x.per);
+    else ssm_step_kernel<T, N, 1><<<grid, 128, 0, st>>>(p, x.per);
     return cudaGetLastError();
 }
 template <typename T>

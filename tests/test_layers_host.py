@@ -249,3 +249,15 @@ def test_sequence_search_in_the_largest_tables(tmp_path):
         free(cu);
     }""")
     assert out == 3 * ["1", "1", "1", "0", "64", "64", "36"]
+
+
+def test_step_covers_the_most_sequences(tmp_path):
+    """How the one-token scan divides sequences among parts: all of them once, up to the most that a call may have."""
+    out = _host_program(tmp_path, """
+    for (int S : {1, 2, 255, 2368, 2369, 0x7fffff00 - 2368, 0x7fffff00})
+        for (int blocks : {1, 3, 384, 2368, 1 << 20}) {
+            const StepParts x = step_parts(S, blocks);
+            const bool all = (long long)x.count * x.per >= S && (long long)(x.count - 1) * x.per < S;
+            printf("%d\\n", all && x.per > 0 && x.count > 0 && x.count <= 65535);
+        }""", "kda_ssm.cuh")
+    assert out == 35 * ["1"]
