@@ -143,8 +143,8 @@ int ssm_dims(const kda_ssm_dims *d, const kda_opts &o, bool step, SsmArgs &a) {
     }
     const int s = check_rows(d->B, (int)a.T, a.cu != nullptr, w, &a.rows);
     if (s != KDA_OK) return s;
-    // states of all sequences, and the seams' states: at most one a sequence and 64 rows
-    if (a.D > 0 && (long long)a.N * (a.S + a.rows / 64 + 1) > kMaxElems / a.D) return KDA_ERR_SHAPE;
+    // states of all sequences, and the seams' states: at most one a sequence and shortest span
+    if (a.D > 0 && (long long)a.N * (a.S + a.rows / kShortestSpan + 1) > kMaxElems / a.D) return KDA_ERR_SHAPE;
     a.bf16 = o.dtype == KDA_BF16;
     return KDA_OK;
 }

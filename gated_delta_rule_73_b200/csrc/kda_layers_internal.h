@@ -43,6 +43,10 @@ cudaError_t launch_short_conv_bwd(const ConvArgs &a, cudaStream_t st);
 // x, y [S, D], state0 -> state_T (may be the same)
 cudaError_t launch_short_conv_step(const ConvArgs &a, cudaStream_t st);
 
+// Rows a span of the selective scan has at least, but the last of a sequence (the backward's; the
+// forward's have 64): what bounds their number, and with it the sizes that a call may have.
+constexpr int kShortestSpan = 16;
+
 struct SsmArgs {
     const void *u, *dt, *Bm, *Cm, *z;    // z nullable
     const float *A, *Dskip, *dt_bias;    // Dskip, dt_bias nullable

@@ -641,7 +641,7 @@ int span_rows(const SsmArgs &a) {
     const long long nblk = (long long)a.G * ((Dg + CH - 1) / CH);
     int best = kSpan;
     double least = 0.0;
-    for (int L = kSpan; L >= 2 * kStep; L -= kStep) {
+    for (int L = kSpan; L >= kShortestSpan; L -= kStep) {
         const long long waves = (span_slots(a.cu != nullptr, a.S, a.T, L) * nblk + 443) / 444;
         const double cost = (double)waves * (L + 24) + 0.25 * (double)(a.T / L);
         if (L == kSpan || cost < least) {

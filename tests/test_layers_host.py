@@ -145,6 +145,15 @@ def test_norm_refusals(L):
 
 
 @host_only
+def test_scan_sizes_are_bounded_by_the_shortest_spans(L):
+    """The seams' states of a backward in spans of 16 rows may be 2^40 values, no more."""
+    rows, D, N = 1 << 27, 2048, 64          # D N rows / 16 = 2^40 - and some for the sequence
+    for d, st in ((_ssm(L, B=1, T=rows, D=D, N=N), SHAPE), (_ssm(L, B=1, T=rows - 4096, D=D, N=N), WORKSPACE)):
+        assert _call(L, "kda_ssm_scan_bwd", 20, d, at=[(i, (i + 1) << 44) for i in range(20)]) == st
+        assert (L._lib.kda_ssm_scan_bwd_workspace_bytes(d, None) == 0) == (st == SHAPE)
+
+
+@host_only
 def test_outputs_over_the_largest_table_of_bounds(L):
     """The table of 2^31 - 1 sequences is 8 GB long, to the call's check of what its outputs overlap as well."""
     n, at = (1 << 31) - 1, 1 << 36
