@@ -358,6 +358,26 @@ def test_ssm_extreme_steps(K):
     assert all(torch.isfinite(o).all() for o in got) and torch.equal(got[8], torch.ones_like(h0))
 
 
+def test_activations_far_out(K):
+    """SiLU and softplus in FP32, each by itself (a tap of 1; no decay, inputs of 1), relative to the value.
+
+    12 + 1.23 |x| half-steps: log2(e) x is rounded (1) with log2(e) itself (0.22), which e^x sees |x| times; the
+    hardware's exponential is off by at most 2^-22 (4) and its reciprocal by 2^-23 (2); a sum, a product, and for
+    softplus the polynomial (2^-27 and 2 roundings), the quotient's product and the last sum make 12 in all.
+    """
+    D, n = 1024, 1 << 20
+    x = torch.linspace(-87, 87, n, dtype=R.F64).float()
+    X = R.d(x)
+    tol = (12 + 1.23 * X.clamp(max=0).abs()) * R.U
+    w = torch.tensor([[0.0, 1.0]]).repeat(D, 1).cuda()
+    y, _ = K.short_conv_fwd(x.view(1, -1, D).cuda(), w)
+    assert ((R.d(y).view(-1) - R.silu(X)).abs() <= tol * R.silu(X).abs()).all()
+    one, B = torch.ones(n // D, 1, D, device="cuda"), torch.ones(n // D, 1, 1, 8, device="cuda")
+    _, h = K.ssm_scan_fwd(one, x.view(-1, 1, D).cuda(), torch.zeros(D, 8, device="cuda"), B, B)
+    ref = torch.log1p(torch.exp(-X.abs())) + X.clamp(min=0)
+    assert ((R.d(h) - ref.view(-1, D, 1)).abs() <= (tol * ref).view(-1, D, 1)).all()
+
+
 # ------------------------------------------------------------------ block norm
 NORM = [
     # rows, D, block, gate, weights, wide
