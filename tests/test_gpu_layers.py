@@ -718,6 +718,106 @@ def test_norm_backward_from_two_threads(K, dtype, monkeypatch):
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
 
 
+def test_offsets_beyond_31_bits_backward_and_steps(K):
+    """The same layout for the gradients and the single tokens, outputs with row strides among them; equal bits."""
+    rows, D, N = 40000, 8, 16
+    wide = torch.empty(1, rows, 70000, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n = lambda *s, dtype=torch.bfloat16: torch.randn(*s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    wide[..., 69000:69000 + 6 * D] = n(1, rows, 6 * D)
+    wide[..., 69500:69500 + 2 * N] = n(1, rows, 2 * N)
+    u, dt, z, dout, out, out2 = (wide[..., 69000 + i * D:69000 + (i + 1) * D] for i in range(6))
+    Bm, Cm = (wide[..., 69500 + i * N:69500 + (i + 1) * N].unflatten(-1, (1, N)) for i in range(2))
+    c = lambda *t: [v.contiguous() for v in t]  # noqa: E731
+    same = lambda a, b: all(torch.equal(p, q) for p, q in zip(a, b) if p is not None)  # noqa: E731
+    w, b = n(D, 4), n(D)
+    dw, db = torch.empty(D, 4, device="cuda"), torch.empty(D, device="cuda")
+    ws = torch.empty(K.kda_short_conv_bwd_workspace_bytes(u, w), dtype=torch.uint8, device="cuda")
+    K.kda_short_conv_bwd(u, w, b, None, dout, None, out, dw, db, None, ws)
+    assert same((out, dw, db), K.short_conv_bwd(*c(u), w, b, None, *c(dout)))
+    K.kda_short_conv_fwd(u, w, b, None, out2, None)
+    assert torch.equal(out2, K.short_conv_fwd(*c(u), w, b)[0])
+    A = -torch.rand(D, N, generator=g, device="cuda") - 0.1
+    K.ssm_scan_fwd(u, dt, A, Bm, Cm, None, z, out=out)
+    assert torch.equal(out, K.ssm_scan_fwd(*c(u, dt), A, *c(Bm, Cm), None, *c(z))[0])
+    assert same(K.ssm_scan_bwd(u, dt, A, Bm, Cm, None, z, None, None, dout),
+                K.ssm_scan_bwd(*c(u, dt), A, *c(Bm, Cm), None, *c(z), None, None, *c(dout)))
+    dres, dx = n(1, rows, D), n(1, rows, D)
+    assert same(K.block_norm_bwd(u, dt, z, None, None, None, dres, dx),
+                K.block_norm_bwd(*c(u, dt, z), None, None, None, dres, dx))
+    # every row a sequence
+    st = n(rows, 3, D)
+    st2 = st.clone()
+    K.short_conv_step(u[0], w, b, st, y=out[0])
+    assert torch.equal(K.short_conv_step(u[0].contiguous(), w, b, st2), out[0]) and torch.equal(st, st2)
+    h = n(rows, D, N, dtype=torch.float32)
+    h2 = h.clone()
+    K.ssm_step(u[0], dt[0], A, Bm[0], Cm[0], None, z[0], None, h, out=out[0])
+    assert torch.equal(K.ssm_step(*c(u[0], dt[0]), A, *c(Bm[0], Cm[0]), None, *c(z[0]), None, h2), out[0])
+    assert torch.equal(h, h2)
+
+
+def test_tensors_of_more_than_31_bits(K):
+    """Contiguous tensors of more than 2^31 values, with the workspaces that they need: a short sequence behind a
+    long one, and the last rows of the norm, against their 64-bit forms."""
+    D, N, long, T = 2048, 32, (1 << 20) + 7, 70
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("about 70 GB of device memory")
+    rows = long + T
+    g = torch.Generator(device="cuda").manual_seed(2)
+    n = lambda *s, dtype=torch.bfloat16: torch.randn(*s, generator=g, device="cuda", dtype=dtype)  # noqa: E731
+    cu = torch.tensor([0, long, rows], dtype=torch.int32, device="cuda")
+    last, bounds = slice(long, rows), [(0, T)]
+    u, dout = n(rows, D), n(rows, D)
+    # the norm: its rows are independent
+    s, wp, wx = (torch.rand(D, generator=g, device="cuda") + 0.3 for _ in range(3))
+    res, x = K.block_norm_fwd(u, dout, None, s, wp, wx)
+    ref = (R.d(u[last]), R.d(dout[last]), None, R.d(s), R.d(wp), R.d(wx))
+    rr, rx = R.norm_fwd(*ref, 1e-5)
+    far = ref[0].abs() + (rr - ref[0]).abs()
+    R.check("res_out", res[last], rr, far, 74)
+    R.check("x", x[last], rx, far * (rx / rr).abs().nan_to_num() + rx.abs(), 74)
+    got = K.block_norm_bwd(res, dout, None, s, wp, wx, x, None)
+    args = (R.d(res[last]), ref[1], None, *ref[3:], R.d(x[last]), None, 1e-5)
+    for name, o, r, f in zip(("dresidual", "dblock"), got, R.norm_bwd(*args), R.norm_bwd(*args, mag=True)):
+        R.check(name, o[last], r, f, 2 * 74)
+    del res, x, got
+    # the convolution
+    w, b, s0 = n(D, 4), n(D), n(2, 3, D)
+    y, sT = K.short_conv_fwd(u, w, b, s0, cu_seqlens=cu)
+    ref = (R.d(u[last]), R.d(w), R.d(b), R.d(s0[1:]))
+    pre, rsT = R.conv_pre(*ref, bounds)
+    far, _ = R.conv_pre(*ref, bounds, mag=True)
+    R.check("y", y[last], R.silu(pre), 1.1 * far + R.silu(pre).abs(), 4 + 48)
+    assert torch.equal(R.d(sT[1:]), rsT)
+    del y
+    dsT = n(2, 3, D, dtype=torch.float32)
+    got = K.short_conv_bwd(u, w, b, s0, dout, dsT, cu_seqlens=cu)
+    args = (*ref, R.d(dout[last]), R.d(dsT[1:]), bounds)
+    want, mag = R.conv_bwd(*args), R.conv_bwd(*args, mag=True)
+    R.check("dx", got[0][last], want[0], mag[0], 4 + 48)
+    R.check("dstate0", got[3][1:], want[3], mag[3], 4 + 48)
+    del got
+    # the scan
+    dt, z = n(rows, D), n(rows, D)
+    Bm, Cm = n(rows, 1, N), n(rows, 1, N)
+    A = -(torch.rand(D, N, generator=g, device="cuda") + 0.05)
+    Ds, bias = n(D, dtype=torch.float32), torch.rand(D, generator=g, device="cuda") * 4 - 5
+    h0, dhT = n(2, D, N, dtype=torch.float32), n(2, D, N, dtype=torch.float32)
+    out, hT = K.ssm_scan_fwd(u, dt, A, Bm, Cm, Ds, z, bias, h0, cu_seqlens=cu)
+    cut = (u[last], dt[last], A, Bm[last], Cm[last], Ds, z[last], bias, h0[1:])
+    (ro, rh), (fo, fh) = _ssm_ref(cut, bounds), _ssm_ref(cut, bounds, mag=True)
+    R.check("out", out[last], ro, fo, 24 * T + N + 64)
+    R.check("h_T", hT[1:], rh, fh, 24 * T + 64)
+    del out
+    got = K.ssm_scan_bwd(u, dt, A, Bm, Cm, Ds, z, bias, h0, dout, dhT, cu_seqlens=cu)
+    more = (R.d(dout[last]), R.d(dhT[1:]))
+    ref, far = _ssm_ref(cut, bounds, *more), _ssm_ref(cut, bounds, *more, mag=True)
+    for i, name in ((0, "du"), (1, "ddt"), (3, "dB"), (4, "dC"), (6, "dz")):
+        R.check(name, got[i][last], ref[i], far[i], 48 * T + N + D + 128)
+    R.check("dh0", got[8][1:], ref[8], far[8], 48 * T + N + D + 128)
+
+
 # ------------------------------------------------------------------ a run of them together
 def _layer_weights(g, dm, D, N, Rk):
     s = lambda *shape: torch.randn(*shape, generator=g, dtype=R.F64) / shape[0] ** 0.5  # noqa: E731
