@@ -12,6 +12,7 @@ import threading
 import pytest
 import torch
 
+from tests import _layers_err as E
 from tests import _layers_ref as R
 
 pytestmark = pytest.mark.gpu
@@ -243,6 +244,28 @@ def test_ssm_scan_forward_and_backward(K, case, dtype):
             continue
         n = 48 * T + N + D + 128 + (rows if name in ("dA", "dDskip", "ddt_bias") else 0)
         R.check(name, o.reshape(r.shape), r, f, n)
+
+
+@pytest.mark.parametrize("lay,D,N,G", [(_dense(1, 1500), 8, 8, 1),                    # spans of time
+                                       (_dense(1, 500), 24, 16, 1),                   # four states a lane
+                                       (_packed([0, 700, 701, 701, 1600], 1600), 6, 16, 2),
+                                       (_packed([0, 900, 1000], 1000), 12, 32, 1)]
+                         if torch.cuda.is_available() else [])
+def test_ssm_error_of_long_sequences(K, lay, D, N, G):
+    """FP32 over long sequences within a running bound of the roundings, which decays as the states do: 60 to 2,000
+    times below a count of all tokens' roundings."""
+    args, cu, bounds, g = _ssm_inputs(lay, D, N, G, True, True, True, True, 0, torch.float32)
+    S = len(bounds)
+    dout, dhT = _n(g, *args[0].shape), _n(g, S, D, N)
+    u, dt, A, Bm, Cm, Ds, z, bias, h0 = args
+    (out, hT), grads = E.ssm(_flat(u), _flat(dt), R.d(A), _flat(Bm, 2), _flat(Cm, 2), R.d(Ds), _flat(z), R.d(bias), R.d(h0),
+                             bounds, _flat(dout), R.d(dhT), 64)
+    got, ghT = K.ssm_scan_fwd(*args, cu_seqlens=cu)
+    E.check("out", got, out)
+    E.check("h_T", ghT, hT)
+    for name, o, w in zip(("du", "ddt", "dA", "dB", "dC", "dDskip", "dz", "ddt_bias", "dh0"),
+                          K.ssm_scan_bwd(*args, dout, dhT, cu_seqlens=cu), grads):
+        E.check(name, o, w)
 
 
 @pytest.mark.parametrize("dtype", DT)

@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from tests import _layers_err as E
 from tests import _layers_ref as R
 
 F64 = torch.float64
@@ -121,3 +122,35 @@ def test_norm_formulas(gated):
         for a, m, f in zip(auto, mine, far):
             assert torch.allclose(a, m, rtol=1e-10, atol=1e-10)
             assert (m.abs() <= f * (1 + 1e-12) + 1e-12).all()
+
+
+@pytest.mark.parametrize("G", [1, 2])
+def test_ssm_running_error_bound(G):
+    """Its values are the plain form's, and FP32 of the plain recursion stays within its bound, by less than 100 times."""
+    g = torch.Generator().manual_seed(G)
+    bounds, rows, D, N = [(0, 150), (150, 151), (151, 151), (151, 300)], 300, 4, 8
+    u, z, dt = _t(g, rows, D), _t(g, rows, D), _t(g, rows, D)
+    A, Bm, Cm = -_t(g, D, N).abs() - 0.1, _t(g, rows, G, N), _t(g, rows, G, N)
+    Ds, bias, h0 = _t(g, D), _t(g, D) - 3, _t(g, 4, D, N)
+    dout, dhT = _t(g, rows, D), _t(g, 4, D, N)
+    single = [v.float() for v in (u, dt, A, Bm, Cm, Ds, z, bias, h0, dout, dhT)]
+    u, dt, A, Bm, Cm, Ds, z, bias, h0, dout, dhT = (v.double() for v in single)
+    args = (u, dt, A, Bm, Cm, Ds, z, bias, h0, bounds)
+    fwd, bwd = E.ssm(*args, dout, dhT, 64)
+    worst = 0.0
+    u, dt, A, Bm, Cm, Ds, z, bias, h0, dout, dhT = single
+    # the plain recursion token by token in FP32
+    out, ends = [], []
+    for s, (lo, hi) in enumerate(bounds):
+        h = h0[s]
+        for t in range(lo, hi):
+            delta = torch.log1p(torch.exp(dt[t] + bias))[:, None]
+            h = torch.exp(delta * A) * h + delta * u[t][:, None] * Bm[t].repeat_interleave(D // G, 0)
+            out.append(((h * Cm[t].repeat_interleave(D // G, 0)).sum(-1) + Ds * u[t]) * R.silu(z[t]))
+        ends.append(h)
+    for name, o, w, r in zip(("out", "h_T"), (torch.stack(out), torch.stack(ends)), fwd, R.ssm(*args)):
+        assert torch.allclose(w.v, r, rtol=1e-12, atol=1e-12)
+        worst = max(worst, E.check(name, o, w))
+    assert worst > 0.01
+    for w, r in zip(bwd, R.ssm(*args, dout.double(), dhT.double())):
+        assert torch.allclose(w.v, r, rtol=1e-11, atol=1e-11)
