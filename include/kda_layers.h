@@ -64,7 +64,8 @@ int kda_short_conv_fwd(const void *x, const void *w, const void *bias, const voi
 /*
  * kda_short_conv_bwd -- gradients of <dy, y> + <dstate_T, state_T> of kda_short_conv_fwd.
  *
- *   dy [rows, D] (activation type); dstate_T [B, K-1, D] FP32 or NULL (zero)
+ *   dy [rows, D] (activation type: FP32 gradients, such as kda_chunk_bwd's, go into an FP32
+ *   call as they are and into a bf16 one rounded); dstate_T [B, K-1, D] FP32 or NULL (zero)
  *   dx [rows, D] (activation type); dw [D, K] FP32; dbias [D] FP32 or NULL to skip;
  *   dstate0 [B, K-1, D] FP32 or NULL to skip
  * opts->workspace: kda_short_conv_bwd_workspace_bytes(dims, opts) bytes.

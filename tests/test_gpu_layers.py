@@ -942,3 +942,60 @@ def test_layer_gradients(K):
     for name, got, want in [("dx", dx, X.grad)] + [(k, grad[k], L[k].grad) for k in grad]:
         err = (R.d(got).reshape(want.shape) - want).abs().max()
         assert err <= 1000 * R.U * max(1.0, float(want.abs().max())), (name, float(err), float(want.abs().max()))
+
+
+def test_delta_rule_layer_gradients(K):
+    """The convolutions ahead of the delta rule and the norm behind it, forward and backward in FP32 (the rule's
+    gradients are FP32: FP32 calls take them as they are), against autograd of the plain layer in 64 bits."""
+    g = torch.Generator().manual_seed(7)
+    B, T, H, d = 2, 33, 2, 64
+    D = H * d
+    s = lambda *shape: torch.randn(*shape, generator=g)  # noqa: E731
+    X = [s(B, T, D) for _ in range(3)]                                # inputs of the three branches
+    W = [torch.rand(D, 4, generator=g) - 0.5 for _ in range(3)]
+    bias = [s(D) * 0.1 for _ in range(3)]
+    decay, beta = -5 * torch.sigmoid(s(B, T, H, d)), torch.sigmoid(s(B, T, H))
+    res, scale, post, pre = s(B, T, D), *(torch.rand(D, generator=g) + 0.5 for _ in range(3))
+    dres, dnxt = s(B, T, D), s(B, T, D)
+    c = lambda v: v.cuda()  # noqa: E731
+    heads = lambda v: v.reshape(B, T, H, d)  # noqa: E731
+
+    qkv = [K.short_conv_fwd(c(x), c(w), c(b))[0] for x, w, b in zip(X, W, bias)]
+    o, _ = K.chunk_fwd(*(heads(v) for v in qkv), c(decay), c(beta))
+    blk = o.reshape(B, T, D)
+    out, nxt = K.block_norm_fwd(c(res), blk, None, c(scale), c(post), c(pre))
+    dr, dblk, *_ = K.block_norm_bwd(out, blk, None, c(scale), c(post), c(pre), c(dres), c(dnxt))
+    dqkv = K.chunk_bwd(*(heads(v) for v in qkv), c(decay), c(beta), None, heads(dblk), want_dS0=False)[:3]
+    got = [K.short_conv_bwd(c(x), c(w), c(b), None, v.reshape(B, T, D)) for x, w, b, v in zip(X, W, bias, dqkv)]
+
+    L = [[R.d(v).requires_grad_() for v in group] for group in (X, W, bias)]
+    zero = torch.zeros(B, 3, D, dtype=R.F64)
+    conv = lambda x, w, b: R.silu(sum(torch.cat([zero, x], 1)[:, j:j + T] * w[:, j] for j in range(4)) + b)  # noqa: E731
+    acts = [conv(x, w, b) for x, w, b in zip(*L)]
+    for a in acts:
+        a.retain_grad()
+    unit = lambda v: v / torch.sqrt((v * v).sum(-1, keepdim=True) + 1e-6)  # noqa: E731
+    q, k, v = (heads(a) for a in acts)
+    q, k = unit(q), unit(k)
+    S, os = torch.zeros(B, H, d, d, dtype=R.F64), []
+    for t in range(T):
+        S = torch.exp(R.d(decay[:, t]))[..., None] * S
+        err = v[:, t] - torch.einsum("bhk,bhkv->bhv", k[:, t], S)
+        S = S + R.d(beta[:, t])[..., None, None] * k[:, t, :, :, None] * err[:, :, None]
+        os.append(torch.einsum("bhk,bhkv->bhv", q[:, t], S))
+    r0 = R.d(res).requires_grad_()
+    fo, fx = R.norm_fwd(r0, torch.stack(os, 1).reshape(B, T, D), None, R.d(scale), R.d(post), R.d(pre), 1e-5)
+    ((fo * R.d(dres)).sum() + (fx * R.d(dnxt)).sum()).backward()
+    assert (R.d(nxt) - fx.detach()).abs().max() <= 1e-4 * fx.detach().abs().max() * 4   # x / rms(x): |r'| <= 4 rms
+    assert (R.d(dr) - r0.grad).abs().max() <= 1e-4 * 4 * r0.grad.abs().max()
+    # The delta rule and its gradients are tested to 1e-4 of the largest value; the gradients of its inputs see
+    # the forward's and the norm's as well (twice that, with the norm's mean three times), and the convolution
+    # passes them on through |silu'| <= 1.1 and four taps of at most 0.5, or sums them over B T rows of inputs
+    for i in range(3):
+        top = acts[i].grad.abs().max()
+        near = 3e-4 * top
+        assert (R.d(dqkv[i]).reshape(B, T, D) - acts[i].grad).abs().max() <= near
+        assert (R.d(got[i][0]) - L[0][i].grad).abs().max() <= near * 1.1 * 2
+        rows = 1.1 * B * T
+        assert (R.d(got[i][1]) - L[1][i].grad).abs().max() <= near * rows * X[i].abs().max()
+        assert (R.d(got[i][2]) - L[2][i].grad).abs().max() <= near * rows
