@@ -14,7 +14,7 @@
 // exchange in shared memory.  Blocks walk the rows, the next row's loads under way while one is
 // computed, with the weights of their columns in registers.  16384 x 2048 in bf16 with a
 // gate: forward 59 us (5.7 TB/s), backward 119 us (4.5 TB/s, 112 with 1 - p as a
-// difference, which loses dgate's precision where the gate is open; issue slots 67 % taken).
+// difference, which loses dgate's precision where the gate is open; issue slots 65 % taken).
 #include "kda_layers_internal.h"
 #include "kda_rows.cuh"
 
@@ -475,7 +475,10 @@ int grid(int rows, int nt, int want) {
     const long long n = 148LL * (k < 1 ? 1 : k > 24 ? 24 : k);
     return rows < n ? rows : (int)n;
 }
-// 16384 x 2048 in bf16: forward 58 us at 768, 71 at 1024, 59 at 1536; backward 108 at 512, 118 at 768
+// 16384 x 2048 in bf16, at 512, 768, 1024 and 1536: forward 68, 59, 72 and 60 us, backward 119, 134, 126 and
+// 133.  2^25 values of other widths, forward at 768: 1024 columns 57 (67 at 512, 70 at 1024), 2048 in FP32 115 (104
+// at 512), 2560 66 and 4096 76 (59 each at 1024: `want / nt` rounded down leaves an SM 640 and 512 threads at
+// 768); backward at 512: 1024 columns 118 (131 at 768), 2560 156 (161), 1028 in FP32 257 (206), 1002 in bf16 190 (172).
 constexpr int kFwdWant = 768, kBwdWant = 512;
 
 template <typename T, int V, int E, int NT, bool WIDE = false>
@@ -515,6 +518,18 @@ cudaError_t launch(const NormArgs &a, bool bwd, cudaStream_t st) {
 
 // E: vectors a thread; NT: the most threads that may make of a block, which sets the registers a
 // thread has.  A row of few has an SM to itself: all the threads that the registers allow.
+// Forward / backward in us, 2^25 values with a gate, and what the neighbouring choice takes:
+//   one vector a thread, up to 256 of them    FP32, 512 columns: 107 / 183, 8 values 116 / 217; bf16 on vectors
+//                                             of 4, 516: 100 / 201, where 8 values take 85 / 189
+//   4 values on vectors of 1 or 2, to 1024    bf16, 1001: 140 / 282, 8 values 171 / 287
+//   8 values, registers of 256 threads, 2048  FP32, 2048: 115 / 198, of 512 threads 119 / 204
+//   8 values, of 512 threads, 4096            FP32, 4096: 106 / 203, of 1024 threads 127 / 359
+//   16 values of 512, bf16 forward, 8192      8192: 59, 8 values of 1024 threads 64, wide 119
+//   8 values, wide, 8192                      FP32, 8192, backward 255, 16 values 347; forward 146, where the row
+//                                             held in registers takes 124 (bf16 on vectors of 4, 4100: 234 and 93)
+//   16 values, wide, all that is left         FP32, 16384: 139 / 250
+// Up to 148 rows a call is short either way: 148 x 2048 in FP32 4.6 / 10.3 with all threads, 5.0 / 10.6 with
+// those of many rows; 148 x 3001 8.3 / 16.5, and 6.2 / 12.7 with those.
 template <typename T, int V>
 cudaError_t launch_v(const NormArgs &a, bool bwd, cudaStream_t st) {
     constexpr int E = 8 / V;
@@ -534,7 +549,7 @@ cudaError_t launch_v(const NormArgs &a, bool bwd, cudaStream_t st) {
 }
 
 // V: the widest vectors, up to 16 bytes, that the width, the row strides and the addresses allow: 8184 x
-// 4100 in bf16 takes 235 us forward and 314 backward on vectors of 4, 526 and 1515 on single values.
+// 4100 in bf16 takes 235 us forward and 320 backward on vectors of 4, 526 and 1515 on single values.
 cudaError_t dispatch(const NormArgs &a, bool bwd, cudaStream_t st) {
     using B = __nv_bfloat16;
     const long long all = a.D | a.ld_res | a.ld_block | a.ld_gate | elements(a.residual, a.bf16) |

@@ -8,9 +8,10 @@
 // (16 results a clock and SM) close behind in bf16.  A thread holds P pairs of neighbouring channels
 // and walks L rows with the K-1 rows before them in registers, so a row is read once by its own walk
 // and K-1 times more, from L2, at the seams.  Neighbouring threads hold neighbouring channels: rows
-// are read in whole sectors.  Pairs go through packed FP32 instructions, which halves the issue slots.  bf16, K = 4: forward 8192 x 12288 in 74 us (5.4 TB/s), backward 16384 x
-// 2048 in 70 us (2.9 TB/s; 69 instructions a pair of channels and row), step 256 x 12288
-// in 8.2 us (6.2 TB/s).
+// are read in whole sectors.  Pairs go through packed FP32 instructions, which halves the issue slots.
+// K = 4: forward 8192 x 12288 in bf16 74 us (5.4 TB/s), in FP32 160 (5.0); backward 16384 x 2048 in
+// bf16 70 (2.9 TB/s; 69 instructions a pair of channels and row), in FP32 88 (4.6); step 256 x 12288
+// in bf16 8.2 (6.2 TB/s).
 #include "kda_layers_internal.h"
 #include "kda_rows.cuh"
 
@@ -454,14 +455,17 @@ ConvP params(const ConvArgs &a, int width) {
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 // Rows a forward walk takes: 64 where that leaves 2^18 threads (the device holds 303,104),
-// down to 8 below.
+// down to 8 below.  In bf16, in us: 8192 x 12288 74 (64 rows; 76 with 32, 78 with 128), 16384 x 2048 31 (32; 35
+// with 16, 31 with 64), 1024 x 2048 6.2 (8; 6.2 with 16 and 32, 9.4 with 64), 3001 x 1001 9.8 (8; 8.3 with 16).
 int fwd_rows(long long rows, int groups) {
     int L = 64;
     while (L > 8 && ceil_div(rows, L) * groups < (1 << 18)) L /= 2;
     return L;
 }
 // Rows a backward walk takes; at least 16, so that the partial sums of (K + 1) FP32 values a
-// channel and walk stay small against the rows' bytes.
+// channel and walk stay small against the rows' bytes.  In bf16, in us: 8192 x 12288 191 (64 rows; 215 with 32,
+// 193 with 128), 16384 x 2048 70 (64; 86 and 77), 4096 x 2048 29 (16; 25 with 32 and 64), 1024 x 2048 14.5 (16; 17
+// with 8, 16.4 with 32), 3001 x 1001 18.5 (16; 17.5 with 32).
 int bwd_rows(long long rows, int D) {
     int L = 64;
     while (L > 16 && ceil_div(rows, L) * (D / 2) < (1 << 18)) L /= 2;

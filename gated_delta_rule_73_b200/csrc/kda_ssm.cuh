@@ -97,9 +97,9 @@ __device__ __forceinline__ SsmBlock ssm_block(const SsmP &a, int CH) {
 
 // 2^x of two values on the FMA pipe, which has room while the special-function unit (16 results a
 // clock and SM) is what the scans wait for.  x = n + f with f in [-1/2, 1/2]; 2^f = 1 + f p(f), p the
-// polynomial of degree 5 through (2^f - 1) / f at its Chebyshev points: the relative error is 2^-26.7
-// anywhere, and that of 2^f - 1 near 0 is 2^-28, which counts where factors close to 1 are multiplied
-// thousands of times.  2^n is put together from n's bits.  Clamped to 2^-127 = 0 and 2^128 = inf;
+// polynomial of degree 5 through (2^f - 1) / f at its Chebyshev points: with the coefficients as they
+// stand its relative error is 2^-26.7 anywhere (2^-23.7 with the roundings of its evaluation), and that of
+// 2^f - 1 near 0 is 2^-28, which counts where factors close to 1 are multiplied thousands of times.  2^n is put together from n's bits.  Clamped to 2^-127 = 0 and 2^128 = inf;
 // NaN stays NaN.
 __device__ __forceinline__ float clamp_exponent(float x) {
     asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x));   // -127

@@ -104,6 +104,8 @@ typedef struct {
  *   u, dt, z, out [rows, D], Bm, Cm [rows, G, N]   activation type (z NULL: no gate)
  *   A [D, N], Dskip [D] or NULL, dt_bias [D] or NULL   FP32
  *   h0 [B, D, N] FP32 or NULL (zero); h_T [B, D, N] FP32, the last states, NULL to skip
+ * A <= 0 and delta >= 0 in earnest: long sequences take products of the factors exp(delta A) over
+ * many tokens, here and in the backward, which have to stay finite in FP32 where factors exceed 1.
  * States and sums are FP32.  opts->workspace: kda_ssm_scan_fwd_workspace_bytes bytes (0 for
  * sizes whose sequences and channels alone fill the device).
  */
