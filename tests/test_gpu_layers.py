@@ -780,7 +780,14 @@ def test_offsets_beyond_31_bits_backward_and_steps(K):
     assert torch.equal(h, h2)
 
 
-def test_tensors_of_more_than_31_bits(K):
+@pytest.fixture
+def memory_back():
+    """Leaves the device's memory to others again."""
+    yield
+    torch.cuda.empty_cache()
+
+
+def test_tensors_of_more_than_31_bits(K, memory_back):
     """Contiguous tensors of more than 2^31 values, with the workspaces that they need: a short sequence behind a
     long one, and the last rows of the norm, against their 64-bit forms."""
     D, N, long, T = 2048, 32, (1 << 20) + 7, 70
